@@ -136,6 +136,14 @@ _sig("engram_wkv_project", [_P, _P, _i64, _P, _P, _i32, _P])
 _sig("engram_wkv_gate_add", [_P, _P, _P, _i32, _P, _P, _i32, _P])
 _sig("engram_gated_residual", [_P, _P, _i64, _P, _i32, _P, _P, _P, _i32, _P])
 _sig("engram_gated_residual_noalloc", [_P, _P, _i64, _P, _i32, _P, _P, _i32, _P])
+_sig("engram_embed", [_P, _i32, _i64, _i32, _i64, _P, _i64, _i32, _i64, ctypes.c_float, _P, _i32, _i64, _i64, _P])
+_sig("engram_embed_grad_workspace", [_i64, _i64, _i32, ctypes.POINTER(_i64)])
+_sig("engram_embed_grad", [_P, _i64, _i32, _i64, _i64, _i32, ctypes.c_float, _P, _i32, _i64, _i64, _i32, _P, _i32,
+                           _i64, _P, _P, _P, _i64, _P])
+_sig("engram_fp8_quantize", [_P, _i32, _i64, _i64, _i64, _i32, _i32, _P, _i64, _P, _P, _i64, _P, _P])
+_sig("engram_fp8_matmul_workspace", [_i64, _i64, _i64, ctypes.POINTER(_i64)])
+_sig("engram_fp8_matmul", [_P, _i64, _P, _P, _i64, _P, _i32, _i32, _i64, _i64, _i64, _P, _i32, _i64, _P, _i64, _P])
+_sig("engram_gate_add_backward", [_P, _P, _P, _P, _i32, _i32, _P, _P, _i32, _P])
 _sig("engram_strerror", [ctypes.c_int], ctypes.c_char_p)
 _sig("engram_host_device_pointer", [_P, ctypes.POINTER(_P)])
 _sig("engram_get_error", [_P])
@@ -719,4 +727,9 @@ def check_device_error(where: str = "device", stream=None):
     _check(engram_get_error(stream), where)
 
 
+from .train_ops import (  # noqa: E402  (needs the functions above)
+    ENGRAM_FP8_SCALE_E8M0, ENGRAM_FP8_SCALE_F32, ENGRAM_GRAD_ACCUMULATE, ENGRAM_GRAD_DENSE, ENGRAM_GRAD_SPARSE,
+    engram_embed, engram_embed_grad, engram_embed_grad_workspace, engram_fp8_matmul, engram_fp8_matmul_workspace,
+    engram_fp8_quantize, engram_gate_add_backward)
 from .runtime import Engram, pad_weight  # noqa: E402  (needs the functions above)
+from .training import SiteTraining  # noqa: E402

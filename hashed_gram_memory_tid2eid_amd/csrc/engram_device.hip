@@ -53,3 +53,8 @@ hipError_t read_and_clear_device_error(hipStream_t stream, int* status) {
 #include "kernels/gemm_packed.hip"
 #include "kernels/gemm_gather.hip"
 #include "kernels/gate.hip"
+#include "kernels/embed.hip"
+#include "kernels/embed_grad.hip"
+#include "kernels/quantize.hip"
+#include "kernels/gemm_fp8.hip"
+#include "kernels/gate_backward.hip"

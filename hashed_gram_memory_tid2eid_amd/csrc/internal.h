@@ -223,6 +223,88 @@ struct GateArgs {
 };
 hipError_t launch_gate_add(const GateArgs& a, hipStream_t stream);
 
+// ---- training operators (train.cpp) -----------------------------------------
+
+// out[t][c seg_pitch + d] = scale * table[ids[t][c]][d] (d < dim), zeros up to seg_pitch.
+struct EmbedArgs {
+  const void* table;     // [rows][table_ld] bf16 or f32
+  int64_t rows, table_ld;
+  int32_t dim, table_f32;
+  const int32_t* ids;    // [T][ids_ld], the first cols of each used
+  int64_t T, ids_ld;
+  int32_t cols;
+  float scale;
+  void* out;             // [T][out_ld] bf16 or f32
+  int32_t out_f32;
+  int64_t out_ld, seg_pitch;
+};
+hipError_t launch_embed(const EmbedArgs& a, hipStream_t stream);
+
+struct EmbedGradArgs {
+  const int32_t* ids;
+  int64_t T, ids_ld;
+  int32_t cols;
+  int64_t rows;
+  int32_t dim;
+  float scale;
+  const void* dout;      // [T][dout_ld] bf16 or f32
+  int32_t dout_f32;
+  int64_t dout_ld, seg_pitch;
+  void* grad;            // [rows][grad_ld] (dense, accumulate) or [T * cols][grad_ld] (sparse)
+  int32_t grad_f32;
+  int64_t grad_ld;
+  int32_t mode;          // engram_grad_mode
+  int32_t* unique;       // sparse: [T * cols]
+  int32_t* count;        // sparse: [1]
+  void* work;
+};
+int64_t embed_grad_workspace_bytes(int64_t n, int64_t rows, int32_t dim);
+hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t stream);
+
+struct QuantizeArgs {
+  const void* x;         // [M][ld] bf16 or f32
+  int32_t x_f32;
+  int64_t M, K, ld;
+  int32_t e8m0;          // scales are e8m0 bytes, else float
+  int32_t block;         // 1: one scale per row and 128 elements; 128: per 128 x 128
+  uint8_t* q;            // [M][q_ld], or null
+  int64_t q_ld;
+  void* s;               // [ceil(K / 128)][M or ceil(M / 128)]
+  uint8_t* qt;           // [K][qt_ld], or null
+  int64_t qt_ld;
+  void* st;              // [ceil(M / 128)][K or ceil(K / 128)]
+};
+hipError_t launch_fp8_quantize(const QuantizeArgs& a, hipStream_t stream);
+
+struct GemmFp8Args {
+  const uint8_t* A;      // e4m3fn [M][lda]
+  const void* sa;        // [KB][M]
+  const uint8_t* B;      // e4m3fn [N][ldb]
+  const void* sb;        // [KB][N] or [KB][ceil(N / 128)]
+  int64_t lda, ldb;
+  int32_t M, N, KB;      // KB: blocks of 128 along k
+  int32_t b_block;       // rows of B that share a scale: 1 or 128
+  int32_t e8m0;
+  void* C;               // [M][ldc] f32 or bf16
+  int32_t c_f32;
+  int64_t ldc;
+  float* work;           // split-K slices
+};
+int64_t gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t KB);
+hipError_t launch_gemm_fp8(const GemmFp8Args& a, hipStream_t stream);
+
+struct GateBackwardArgs {
+  const float* v;        // [T][hidden]
+  const void* x;         // bf16 [T][hc][hidden], the streams before the add
+  const void* dy;        // bf16 [T][hc][hidden]
+  const uint8_t* keep;   // [T] or NULL
+  void* dx;              // bf16 [T][hc][hidden]
+  float* dv;             // [T][hidden]
+  int32_t T, hidden;
+  float inv_sqrt_hidden;
+};
+hipError_t launch_gate_backward(const GateBackwardArgs& a, hipStream_t stream);
+
 // The wkv handle's dispatch (abi.cpp), shared by the entry points that bring their
 // own scratch: the argument check of a T-token call, its plan, the planned
 // projection into d_v or the split-K slices at d_partials, and the gated add from

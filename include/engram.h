@@ -537,6 +537,105 @@ int engram_gated_residual_noalloc(const engram_layout* layout, const void* d_row
                                   const engram_wkv* wkv, int32_t hc_mult, const uint8_t* d_keep,
                                   void* d_streams, int32_t T, hipStream_t stream);
 
+/* ---- training operators ------------------------------------------------------ */
+/* What a training or fine-tuning step of an Engram site needs beside the forward path:
+ * a lookup into a trainable table and its gradient, 8-bit products with block scales for
+ * the projection (its forward, also for single tokens, and both its gradients), and the
+ * gate's backward pass.  They are bound to no layout.  All are hot calls: nothing is
+ * allocated, nothing synchronises, every launch goes to `stream` and may be captured;
+ * scratch is the caller's.  No sum is made by atomics: the same call gives the same bits.
+ * Pointers are aligned to their element unless said otherwise; aligning rows to 16 bytes
+ * is faster. */
+
+/* The lookup: out[t][c * seg_pitch + d] = scale * table[ids[t * ids_ld + c]][d] for
+ * d < dim, zeros for d in [dim, seg_pitch); the fp32 product is rounded once to out_dtype.
+ * An id of -1 gives zeros.
+ *   d_table [rows][table_ld] BF16 or F32 (rows < 2^31), d_ids int32 [T][ids_ld] of which
+ *   the first `cols` are looked up, d_out [T][out_ld] BF16 or F32, out_ld >= cols *
+ *   seg_pitch, seg_pitch >= dim; scale finite.
+ * Row ids of engram_compress_hash are such ids: cols 3 * H for one table per site, or H
+ * for each order's own table (ids and out then start at the order's columns).
+ * Host errors: ENGRAM_E_ARG, ENGRAM_E_ALIGN, ENGRAM_E_UNSUPPORTED (cols * seg_pitch or T
+ * past 2^31).  Device error: ENGRAM_E_ROW_RANGE (an id other than -1 outside the table;
+ * its segment is zero). */
+int engram_embed(const void* d_table, int32_t table_dtype, int64_t rows, int32_t dim, int64_t table_ld,
+                 const int32_t* d_ids, int64_t T, int32_t cols, int64_t ids_ld, float scale, void* d_out,
+                 int32_t out_dtype, int64_t out_ld, int64_t seg_pitch, hipStream_t stream);
+
+/* Where the lookup's gradient goes. */
+typedef enum engram_grad_mode {
+  ENGRAM_GRAD_DENSE = 0,      /* every row of grad [rows][grad_ld] is written, zero where no id named it */
+  ENGRAM_GRAD_ACCUMULATE = 1, /* rows that were looked up are added to; the others stay (with scale = -rate
+                                 on the table itself, this is the update of plain gradient descent) */
+  ENGRAM_GRAD_SPARSE = 2      /* one row per distinct id, ids ascending, in grad [T * cols][grad_ld];
+                                 rows past the count are not written */
+} engram_grad_mode;
+
+/* The lookup's gradient: G[r][d] = scale * sum of dout[t][c * seg_pitch + d] over the
+ * places (t, c) with ids[t * ids_ld + c] = r, summed in fp32 in an order fixed by the
+ * ids, rounded once to grad_dtype.
+ *   d_dout [T][dout_ld] BF16 or F32; T * cols <= 2^30; d_grad by `mode`, BF16 or F32.
+ *   SPARSE: d_unique int32 [T * cols] receives the distinct ids, then -1; d_count int32
+ *   [1] their number.
+ *   d_work: engram_embed_grad_workspace(T * cols, rows, dim) bytes, 256-byte aligned.
+ * Host errors: ENGRAM_E_ARG, ENGRAM_E_ALIGN, ENGRAM_E_SCRATCH, ENGRAM_E_UNSUPPORTED.
+ * Device error: ENGRAM_E_ROW_RANGE (such an id counts as -1: it has no gradient). */
+int engram_embed_grad_workspace(int64_t places, int64_t rows, int32_t dim, int64_t* bytes);
+int engram_embed_grad(const int32_t* d_ids, int64_t T, int32_t cols, int64_t ids_ld, int64_t rows, int32_t dim,
+                      float scale, const void* d_dout, int32_t dout_dtype, int64_t dout_ld, int64_t seg_pitch,
+                      int32_t mode, void* d_grad, int32_t grad_dtype, int64_t grad_ld, int32_t* d_unique,
+                      int32_t* d_count, void* d_work, int64_t work_bytes, hipStream_t stream);
+
+/* Scales of 8-bit operands. */
+typedef enum engram_fp8_scale {
+  ENGRAM_FP8_SCALE_F32 = 0, /* float: max(amax / 448, 2^-126), rounded once             */
+  ENGRAM_FP8_SCALE_E8M0 = 1 /* uint8 e8m0: the least power of two not below that float  */
+} engram_fp8_scale;
+
+/* Quantises x [M][x_ld] (BF16 or F32, K columns) to e4m3fn codes with one scale s per
+ * block: code = e4m3fn(fl32(x / s)), nearest even.
+ *   block_rows 1:   d_q [M][q_ld], d_scales [ceil(K/128)][M]: blocks of 1 x 128 along the row;
+ *                   d_qt [K][qt_ld], d_scales_t [ceil(M/128)][K]: the transpose, blocks of 128
+ *                   along the column of x.
+ *   block_rows 128: blocks of 128 x 128; d_scales [ceil(K/128)][ceil(M/128)], d_scales_t its
+ *                   transpose [ceil(M/128)][ceil(K/128)].
+ * Either pair may be NULL, not both; both come from one pass over x.  q_ld (qt_ld) is at
+ * least K (M) rounded up to 128 and a multiple of 16, d_q and d_qt 16-byte aligned; codes
+ * from K (M) up to that multiple of 128 are written as zero.  A block that holds an
+ * infinity or a NaN becomes all NaN.
+ * Host errors: ENGRAM_E_ARG, ENGRAM_E_ALIGN, ENGRAM_E_UNSUPPORTED. */
+int engram_fp8_quantize(const void* d_x, int32_t x_dtype, int64_t M, int64_t K, int64_t x_ld, int32_t scale_kind,
+                        int32_t block_rows, uint8_t* d_q, int64_t q_ld, void* d_scales, uint8_t* d_qt, int64_t qt_ld,
+                        void* d_scales_t, hipStream_t stream);
+
+/* C[m][n] = sum over k of a[m][k] b[n][k], for operands of engram_fp8_quantize: the value
+ * of a code is its scale times its e4m3fn value.  Accumulated in fp32, rounded once to
+ * c_dtype (BF16 or F32).
+ *   d_a [M][a_ld] codes with scales d_sa [K/128][M]; d_b [N][b_ld] codes with scales d_sb
+ *   [K/128][N] (b_block_rows 1) or [K/128][ceil(N/128)] (b_block_rows 128); both scales of
+ *   scale_kind.  K a multiple of 128 (codes past the matrix are zero); a_ld, b_ld >= K,
+ *   multiples of 16, rows 16-byte aligned; d_c [M][c_ld].
+ *   Scales are multiplied before they meet a sum: their products must be finite.
+ *   d_work: engram_fp8_matmul_workspace(M, N, K) bytes (0 unless K is split over
+ *   workgroups, which few rows need), 16-byte aligned.
+ * Host errors: ENGRAM_E_ARG, ENGRAM_E_ALIGN, ENGRAM_E_SCRATCH, ENGRAM_E_UNSUPPORTED (256
+ * rows of codes past 2^31 bytes). */
+int engram_fp8_matmul_workspace(int64_t M, int64_t N, int64_t K, int64_t* bytes);
+int engram_fp8_matmul(const uint8_t* d_a, int64_t a_ld, const void* d_sa, const uint8_t* d_b, int64_t b_ld,
+                      const void* d_sb, int32_t b_block_rows, int32_t scale_kind, int64_t M, int64_t N, int64_t K,
+                      void* d_c, int32_t c_dtype, int64_t c_ld, void* d_work, int64_t work_bytes, hipStream_t stream);
+
+/* Backward pass of engram_gate_add: from v, the streams x before the add, keep and the
+ * gradient dy of the streams after it,
+ *   z_s = <x_s, v> / sqrt(hidden), g_s = sigmoid(z_s),
+ *   e_s = <dy_s, v> g_s (1 - g_s) / sqrt(hidden),
+ *   dx_s = bf16(dy_s + keep e_s v),  dv = keep sum_s (g_s dy_s + e_s x_s).
+ * d_v, d_dv float [T][hidden]; d_streams, d_dy, d_dx bf16 [T][hc_mult][hidden], all
+ * 16-byte aligned; d_keep uint8 [T] or NULL.  d_dx may be d_dy.  keep 0 passes dy through
+ * bit for bit and gives dv = 0.  Errors as engram_gate_add. */
+int engram_gate_add_backward(const float* d_v, const void* d_streams, const uint8_t* d_keep, const void* d_dy,
+                             int32_t hidden, int32_t hc_mult, void* d_dx, float* d_dv, int32_t T, hipStream_t stream);
+
 /* ---- errors ------------------------------------------------------------- */
 const char* engram_strerror(int status);
 /* Synchronises `stream`, returns the first device-detected status latched on

@@ -1,0 +1,642 @@
+"""The training operators against their definitions in 64 bits.
+
+Tolerances, fixed from the arithmetic before any run:
+- a lookup is one fp32 product rounded once: compared bit for bit;
+- a sum of L fp32 terms is off by at most L 2^-24 times the sum of their magnitudes (each of
+  its L additions rounds by at most 2^-24 of a partial sum), the scale and the output's
+  rounding add 2^-24 and half a step of the type;
+- codes and scales follow from single correctly rounded operations: compared bit for bit;
+- an fp32 product's matrix instruction may drop bits below 2^-24 of its largest term instead of
+  rounding, so a step of its accumulation counts 2^-23; products of small whole numbers with
+  power-of-two scales are exact and compared bit for bit.  A bf16 product's 8-bit instruction
+  adds groups of up to 8 neighbouring products and keeps 15 bits or more below a group's
+  largest: what it drops is at most 8 * 2^-15 of each group's magnitudes.
+"""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16, F32 = torch.bfloat16, torch.float32
+HALF = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
+E24 = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def eng():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU visible")
+    import hashed_gram_memory_tid2eid_amd as e
+    return e
+
+
+@pytest.fixture(autouse=True)
+def no_device_error(request):
+    yield
+    if torch.cuda.is_available():
+        import hashed_gram_memory_tid2eid_amd as e
+        assert e.engram_get_error() == 0
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *shape, dtype=F32, std=1.0):
+    return (torch.randn(shape, generator=g, device=DEV) * std).to(dtype)
+
+
+def same_bits(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+def guarded(rows, cols, dtype, lead=3, extra=5):
+    """A rows x cols view inside a larger buffer of a known fill, and the check that nothing around
+    the view changed."""
+    whole = torch.full((rows + 2, lead + cols + extra), 77.0, dtype=dtype, device=DEV)
+    view = whole[1:1 + rows, lead:lead + cols]
+
+    def untouched():
+        w = whole.float().clone()
+        w[1:1 + rows, lead:lead + cols] = 77.0
+        return bool((w == 77.0).all())
+    return view, untouched
+
+
+# ---------------------------------------------------------------------------
+# lookup
+# ---------------------------------------------------------------------------
+
+def embed_ref(table, ids, scale, seg, dtype):
+    rows = table.double()[ids.long().clamp_min(0)] * float(torch.tensor(scale, dtype=F32))
+    rows = torch.where(ids[..., None] < 0, 0.0, rows)
+    return torch.nn.functional.pad(rows, (0, seg - table.shape[1])).float().to(dtype).flatten(1)
+
+
+@pytest.mark.parametrize("T, cols, dim, seg", [
+    (1, 1, 1, 1), (1, 24, 256, 256), (3, 3, 130, 192), (17, 6, 128, 128), (5, 2, 7, 8), (4, 1, 4096, 4096),
+    (300, 24, 256, 256), (2000, 24, 256, 256), (33, 3, 6500, 6528), (9, 5, 13, 17)])
+@pytest.mark.parametrize("table_dtype", [BF16, F32])
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+def test_embed(eng, T, cols, dim, seg, table_dtype, out_dtype):
+    g = gen(T * 31 + dim)
+    table = randn(g, 257, dim, dtype=table_dtype)
+    ids = torch.randint(-1, 257, (T, cols), generator=g, device=DEV, dtype=torch.int32)
+    out = torch.full((T, cols * seg), 5.0, dtype=out_dtype, device=DEV)
+    eng.engram_embed(table, ids, out, scale=1.7, seg_pitch=seg)
+    assert same_bits(out, embed_ref(table, ids, 1.7, seg, out_dtype) + 0.0)
+
+
+def test_embed_strided_views(eng):
+    g = gen(1)
+    table = randn(g, 60, 103, dtype=BF16)[:, 3:99]  # 96 wide, rows not on 16 bytes
+    ids = torch.randint(-1, 60, (40, 9), generator=g, device=DEV, dtype=torch.int32)[:, 2:5]
+    out, untouched = guarded(40, 3 * 96, F32)
+    eng.engram_embed(table, ids, out, scale=-0.25)
+    assert torch.equal(out, embed_ref(table, ids, -0.25, 96, F32)) and untouched()
+
+
+def test_embed_rows_past_32_bit_offsets(eng):
+    # the last rows of a table of 4.4 GB: element offsets past 2^31
+    table = torch.zeros((540_000, 4096), dtype=BF16, device=DEV)
+    ids = torch.tensor([539_999, 0, 524_288, 539_998], dtype=torch.int32, device=DEV)
+    table[ids.long()] = randn(gen(2), 4, 4096, dtype=BF16)
+    out = torch.empty((4, 4096), dtype=BF16, device=DEV)
+    eng.engram_embed(table, ids, out)
+    assert same_bits(out, table[ids.long()])
+
+
+def test_embed_bad_id_latches_and_gives_zeros(eng):
+    table = torch.ones((10, 64), device=DEV)
+    ids = torch.tensor([3, 10, -2, 4], dtype=torch.int32, device=DEV)
+    out = torch.full((4, 64), 9.0, device=DEV)
+    eng.engram_embed(table, ids, out)
+    assert eng.engram_get_error() == eng.ENGRAM_E_ROW_RANGE
+    assert out.sum(1).tolist() == [64.0, 0.0, 0.0, 64.0]
+
+
+# ---------------------------------------------------------------------------
+# lookup gradient
+# ---------------------------------------------------------------------------
+
+def grad_ref(ids, dout, rows, dim, seg, scale):
+    """float64 gradient, the sum of magnitudes behind each value, and the number of terms of each row."""
+    ids = ids.long().flatten()
+    live = (ids >= 0) & (ids < rows)
+    d = dout.reshape(ids.numel(), seg)[live][:, :dim].double() * float(torch.tensor(scale, dtype=F32))
+    out = torch.zeros((rows, dim), dtype=torch.float64, device=DEV).index_add_(0, ids[live], d)
+    mag = torch.zeros((rows, dim), dtype=torch.float64, device=DEV).index_add_(0, ids[live], d.abs())
+    return out, mag, torch.bincount(ids[live], minlength=rows)
+
+
+def grad_ok(got, ref, mag, terms, start=None):
+    """|got - ref| within the terms' additions, the scale, and the rounding to got's type."""
+    tol = (terms[:, None] + 2) * E24 * mag + HALF[got.dtype] * ref.abs() * 1.01 + 1e-40
+    if start is not None:
+        tol = tol + (E24 + HALF[got.dtype]) * (start.double().abs() + mag)
+    return bool(((got.double() - ref).abs() <= tol).all())
+
+
+def run_grad(eng, ids, dout, rows, dim, seg, scale, mode, dtype, start=None):
+    n = ids.numel()
+    work = torch.empty(eng.engram_embed_grad_workspace(n, rows, dim), dtype=torch.uint8, device=DEV)
+    if mode == "sparse":
+        grad = torch.full((n, dim), 3.0, dtype=dtype, device=DEV)
+        unique = torch.full((n,), -7, dtype=torch.int32, device=DEV)
+        count = torch.full((1,), -7, dtype=torch.int32, device=DEV)
+        eng.engram_embed_grad(ids, dout, grad, rows=rows, scale=scale, mode=mode, seg_pitch=seg, unique=unique, count=count,
+                              workspace=work)
+        return grad, unique, int(count)
+    grad = torch.full((rows, dim), 3.0, dtype=dtype, device=DEV) if start is None else start.clone()
+    eng.engram_embed_grad(ids, dout, grad, rows=rows, scale=scale, mode=mode, seg_pitch=seg, workspace=work)
+    return grad
+
+
+SHAPES = [(1, 1, 1, 1, 8), (1, 1, 1, 64, 64), (3, 2, 5, 7, 8), (40, 3, 9, 130, 192), (65, 24, 300, 256, 256),
+          (512, 6, 4096, 128, 128), (1000, 1, 70_000, 96, 96), (2049, 1, 3, 16, 16), (4096, 1, 5, 64, 64),
+          (8000, 5, 20_000_000, 24, 24), (333, 1, 129_280, 2056, 2056), (700, 2, 50, 13, 17), (5, 1, 40, 4096, 4096)]
+
+
+@pytest.mark.parametrize("T, cols, rows, dim, seg", SHAPES)
+@pytest.mark.parametrize("dout_dtype, dtype", [(BF16, F32), (F32, BF16), (F32, F32)])
+def test_embed_grad_sparse(eng, T, cols, rows, dim, seg, dout_dtype, dtype):
+    g = gen(T + dim)
+    ids = torch.randint(-1, rows, (T, cols), generator=g, device=DEV, dtype=torch.int32)
+    dout = randn(g, T, cols * seg, dtype=dout_dtype)
+    grad, unique, count = run_grad(eng, ids, dout, rows, dim, seg, 0.7, "sparse", dtype)
+    names, inverse = torch.unique(ids[ids >= 0].long(), return_inverse=True)
+    assert count == names.numel()
+    assert torch.equal(unique[:count].long(), names) and bool((unique[count:] == -1).all())
+    assert bool((grad[count:] == 3.0).all())
+    if count == 0:
+        return
+    small = torch.full((T, cols), -1, dtype=torch.int32, device=DEV)
+    small[ids >= 0] = inverse.int()
+    ref, mag, terms = grad_ref(small, dout, count, dim, seg, 0.7)
+    assert grad_ok(grad[:count], ref, mag, terms)
+
+
+@pytest.mark.parametrize("T, cols, rows, dim, seg", [s for s in SHAPES if s[2] < 1_000_000])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_embed_grad_dense_and_accumulate(eng, T, cols, rows, dim, seg, dtype):
+    g = gen(T + dim + 1)
+    ids = torch.randint(-1, rows, (T, cols), generator=g, device=DEV, dtype=torch.int32)
+    dout = randn(g, T, cols * seg, dtype=BF16)
+    ref, mag, terms = grad_ref(ids, dout, rows, dim, seg, -1.3)
+    grad = run_grad(eng, ids, dout, rows, dim, seg, -1.3, "dense", dtype)
+    assert grad_ok(grad, ref, mag, terms)
+    assert bool((grad[terms == 0] == 0).all())
+    start = randn(g, rows, dim, dtype=dtype)
+    added = run_grad(eng, ids, dout, rows, dim, seg, -1.3, "accumulate", dtype, start)
+    assert grad_ok(added, ref + start.double(), mag, terms, start)
+    assert same_bits(added[terms == 0], start[terms == 0])
+
+
+@pytest.mark.parametrize("n", [1, 7, 8, 9, 255, 256, 257, 4095, 4096, 4097, 32_768, 32_769, 70_001])
+@pytest.mark.parametrize("kind", ["one", "runs", "none", "last"])
+def test_embed_grad_long_runs(eng, n, kind):
+    """One row for every place, runs of every length around the chunk sizes, no live place at all,
+    and a single live place behind dead ones.  Whole numbers: sums are exact in any order."""
+    rows, dim = 4000, 24
+    i = torch.arange(n, device=DEV)
+    if kind == "one":
+        ids = torch.full((n,), 17, device=DEV)
+    elif kind == "runs":
+        ids = (torch.sqrt(2.0 * i.double()).long()) % rows  # runs of 1, 2, 3, ... places
+    elif kind == "none":
+        ids = torch.full((n,), -1, device=DEV)
+    else:
+        ids = torch.where(i == n - 1, rows - 1, -1)
+    order = torch.randperm(n, generator=gen(n), device=DEV)
+    ids = ids[order].int().view(n, 1)
+    dout = torch.randint(-4, 5, (n, dim), generator=gen(n + 1), device=DEV).to(BF16)
+    ref, _, terms = grad_ref(ids, dout, rows, dim, dim, 2.0)
+    assert torch.equal(run_grad(eng, ids, dout, rows, dim, dim, 2.0, "dense", F32).double(), ref)
+    grad, unique, count = run_grad(eng, ids, dout, rows, dim, dim, 2.0, "sparse", F32)
+    assert count == int((terms > 0).sum())
+    assert torch.equal(grad[:count].double(), ref[terms > 0])
+    assert torch.equal(unique[:count].long(), torch.nonzero(terms).flatten())
+
+
+def test_embed_grad_repeats_bit_for_bit_and_ignores_the_workspace(eng):
+    g = gen(5)
+    ids = torch.randint(0, 40, (3000, 2), generator=g, device=DEV, dtype=torch.int32)
+    dout = randn(g, 3000, 2 * 64)
+    first = run_grad(eng, ids, dout, 40, 64, 64, 1.0, "dense", F32)
+    for fill in (0, 255):
+        work = torch.full((eng.engram_embed_grad_workspace(6000, 40, 64),), fill, dtype=torch.uint8, device=DEV)
+        again = torch.empty_like(first)
+        eng.engram_embed_grad(ids, dout, again, rows=40, seg_pitch=64, workspace=work)
+        assert same_bits(first, again)
+
+
+def test_embed_grad_strided_views(eng):
+    g = gen(6)
+    ids = torch.randint(-1, 30, (50, 8), generator=g, device=DEV, dtype=torch.int32)[:, 3:6]
+    dout = randn(g, 50, 400, dtype=BF16)[:, 5:5 + 3 * 96]
+    grad, untouched = guarded(30, 96, F32)
+    work = torch.empty(eng.engram_embed_grad_workspace(150, 30, 96), dtype=torch.uint8, device=DEV)
+    eng.engram_embed_grad(ids, dout, grad, rows=30, workspace=work)
+    ref, mag, terms = grad_ref(ids, dout, 30, 96, 96, 1.0)
+    assert grad_ok(grad, ref, mag, terms) and untouched()
+
+
+def test_embed_grad_bad_ids_and_no_places(eng):
+    ids = torch.tensor([1, 9, -5, 1], dtype=torch.int32, device=DEV)
+    dout = torch.ones((4, 8), device=DEV)
+    grad = run_grad(eng, ids, dout, 9, 8, 8, 1.0, "dense", F32)
+    assert eng.engram_get_error() == eng.ENGRAM_E_ROW_RANGE
+    assert grad.sum(1).tolist() == [0.0, 16.0] + [0.0] * 7
+    none = ids[:0]
+    assert bool((run_grad(eng, none, dout[:0], 9, 8, 8, 1.0, "dense", F32) == 0).all())
+    _, _, count = run_grad(eng, none, dout[:0], 9, 8, 8, 1.0, "sparse", F32)
+    assert count == 0
+
+
+def test_embed_grad_infinities_stay_in_their_row(eng):
+    ids = torch.tensor([0, 1, 1, 2, -1], dtype=torch.int32, device=DEV)
+    dout = torch.ones((5, 8), device=DEV)
+    dout[1, 3], dout[3, 4], dout[4] = float("inf"), float("nan"), float("nan")
+    grad = run_grad(eng, ids, dout, 4, 8, 8, 1.0, "dense", F32)
+    want = torch.zeros(4, 8, device=DEV)
+    want[0], want[1], want[2] = 1.0, 2.0, 1.0
+    want[1, 3], want[2, 4] = float("inf"), float("nan")
+    assert torch.equal(torch.nan_to_num(grad, nan=-9.0), torch.nan_to_num(want, nan=-9.0))
+
+
+def test_embed_grad_is_the_adjoint_of_embed(eng):
+    """<embed(table + d) - embed(table), dout> = <d, grad>: the lookup is linear, so the difference is
+    exact; whole numbers keep every sum exact."""
+    g = gen(8)
+    ids = torch.randint(-1, 50, (200, 3), generator=g, device=DEV, dtype=torch.int32)
+    d = torch.randint(-3, 4, (50, 40), generator=g, device=DEV).float()
+    dout = torch.randint(-3, 4, (200, 3 * 64), generator=g, device=DEV).float()
+    out = torch.empty((200, 3 * 64), device=DEV)
+    eng.engram_embed(d, ids, out, scale=4.0, seg_pitch=64)
+    grad = run_grad(eng, ids, dout, 50, 40, 64, 4.0, "dense", F32)
+    assert float((out.double() * dout.double()).sum()) == float((grad.double() * d.double()).sum())
+
+
+# ---------------------------------------------------------------------------
+# quantiser
+# ---------------------------------------------------------------------------
+
+def up(n):
+    return -(-n // 128) * 128
+
+
+def quantize_ref(x, e8m0, block=1):
+    """Codes [M][up(K)] and float scales [K/128][M or M/128], on the host in single operations."""
+    x = x.float().cpu()
+    M, K = x.shape
+    rows = up(M) if block == 128 else M
+    wide = torch.zeros((rows, up(K)))
+    wide[:M, :K] = x
+    t = wide.view(rows // block, block, -1, 128)
+    amax = t.abs().amax(dim=(1, 3))
+    s = torch.maximum(amax / torch.tensor(448.0), torch.tensor(2.0 ** -126))
+    if e8m0:
+        s = torch.exp2(torch.ceil(torch.log2(s.double()))).float()
+    q = (t / s[:, None, :, None]).to(torch.float8_e4m3fn).view(rows, -1)[:M]
+    return q, s.t().contiguous()
+
+
+def held(s, e8m0):
+    return (s.view(torch.int32) >> 23).to(torch.uint8) if e8m0 else s
+
+
+def rough(g, M, K, dtype):
+    """Rows and columns of very different size, with zero blocks and ties."""
+    x = torch.randn((M, K), generator=g, device=DEV) * torch.exp(3 * torch.randn((M, 1), generator=g, device=DEV))
+    x[:, K // 2:K // 2 + 130] = 0.0
+    x[M // 2, :] = torch.round(x[M // 2, :] * 4) / 4
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("M, K", [(1, 1), (1, 128), (3, 130), (16, 256), (17, 8), (128, 128), (129, 255), (300, 1000),
+                                  (2500, 384), (77, 6144)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("e8m0", [False, True])
+@pytest.mark.parametrize("block", [1, 128])
+def test_quantize(eng, M, K, dtype, e8m0, block):
+    x = rough(gen(M + K), M, K, dtype)
+    kind = torch.uint8 if e8m0 else F32
+    want_q, want_s = quantize_ref(x, e8m0, block)
+    want_t, want_st = quantize_ref(x.t(), e8m0, block)
+    for rows, cols in ((True, True), (True, False), (False, True)):
+        q = torch.full((M, up(K) + 16), 9, dtype=torch.uint8, device=DEV) if rows else None
+        s = torch.empty(want_s.shape, dtype=kind, device=DEV) if rows else None
+        qt = torch.full((K, up(M) + 32), 9, dtype=torch.uint8, device=DEV) if cols else None
+        st = torch.empty(want_st.shape, dtype=kind, device=DEV) if cols else None
+        eng.engram_fp8_quantize(x, q, s, q_t=qt, scales_t=st, block_rows=block)
+        for got, sc, wq, ws in ((q, s, want_q, want_s), (qt, st, want_t, want_st)):
+            if got is None:
+                continue
+            assert torch.equal(sc.cpu(), held(ws, e8m0))
+            n = wq.shape[1]
+            # -0 and 0 are one value
+            assert torch.equal(got[:, :n].cpu().view(torch.float8_e4m3fn).float(), wq.float())
+            assert bool((got[:, n:] == 9).all())
+
+
+def test_quantize_strided_input(eng):
+    x = rough(gen(3), 40, 300, BF16)[:, 7:7 + 200]
+    q, s = torch.empty((40, 256), dtype=torch.float8_e4m3fn, device=DEV), torch.empty((2, 40), device=DEV)
+    eng.engram_fp8_quantize(x, q, s)
+    wq, ws = quantize_ref(x, False)
+    assert torch.equal(s.cpu(), ws) and torch.equal(q.cpu().float(), wq.float())
+
+
+@pytest.mark.parametrize("e8m0", [False, True])
+def test_quantize_extremes(eng, e8m0):
+    """Magnitudes at both ends of fp32: the smallest scale is 2^-126, the largest values do not overflow."""
+    x = torch.zeros((6, 128), device=DEV)
+    x[0, 5] = 3.4028234e38
+    x[1, 5] = 1e-45
+    x[2, 5], x[2, 6] = 448.0 * 2.0 ** -126, -(2.0 ** -126)
+    x[3, 5] = -448.0
+    x[4, 5] = 448.0 * (1 + 2.0 ** -23)
+    q = torch.empty((6, 128), dtype=torch.float8_e4m3fn, device=DEV)
+    s = torch.empty((1, 6), dtype=torch.uint8 if e8m0 else F32, device=DEV)
+    eng.engram_fp8_quantize(x, q, s)
+    wq, ws = quantize_ref(x, e8m0)
+    assert torch.equal(s.cpu(), held(ws, e8m0)) and torch.equal(q.cpu().float(), wq.float())
+
+
+@pytest.mark.parametrize("e8m0", [False, True])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_quantize_non_finite_blocks_are_nan(eng, e8m0, bad):
+    x = torch.ones((130, 256), device=DEV)
+    x[3, 7] = bad
+    q, qt = (torch.empty(s, dtype=torch.float8_e4m3fn, device=DEV) for s in ((130, 256), (256, 256)))
+    kind = torch.uint8 if e8m0 else F32
+    s, st = torch.empty((2, 130), dtype=kind, device=DEV), torch.empty((2, 256), dtype=kind, device=DEV)
+    eng.engram_fp8_quantize(x, q, s, q_t=qt, scales_t=st)
+    nan, nan_t = q.float().isnan(), qt.float().isnan()
+    assert bool(nan[3, :128].all()) and int(nan.sum()) == 128
+    assert bool(nan_t[7, :128].all()) and int(nan_t.sum()) == 128
+
+
+# ---------------------------------------------------------------------------
+# product
+# ---------------------------------------------------------------------------
+
+def deq(q, s, block=1):
+    """float64 values of codes and scales."""
+    s = s.double() if s.dtype == F32 else torch.exp2(s.double() - 127)
+    r = torch.arange(q.shape[0], device=q.device) // block
+    return (q.double().view(q.shape[0], -1, 128) * s.t()[r][:, :, None]).flatten(1)
+
+
+def operand(g, rows, K, e8m0, block, whole=False):
+    """Codes and scales of an operand whose K is whole blocks; small whole numbers and power-of-two
+    scales when `whole`."""
+    n = rows if block == 1 else -(-rows // 128)
+    if whole:
+        q = torch.randint(-3, 4, (rows, K), generator=g, device=DEV).float().to(torch.float8_e4m3fn)
+        e = torch.randint(-2, 3, (K // 128, n), generator=g, device=DEV)
+        s = (e + 127).to(torch.uint8) if e8m0 else torch.exp2(e.float())
+        return q, s
+    q = (torch.randn((rows, K), generator=g, device=DEV) * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+    s = torch.exp(torch.randn((K // 128, n), generator=g, device=DEV))
+    if e8m0:
+        s = torch.randint(120, 134, (K // 128, n), generator=g, device=DEV).to(torch.uint8)
+    return q, s
+
+
+def product(eng, a, sa, b, sb, out):
+    need = eng.engram_fp8_matmul_workspace(a.shape[0], b.shape[0], a.shape[1])
+    work = torch.empty(need, dtype=torch.uint8, device=DEV) if need else None
+    eng.engram_fp8_matmul(a, sa, b, sb, out, workspace=work)
+    return out
+
+
+PRODUCTS = [(1, 1, 128), (1, 4096, 6144), (2, 8, 256), (5, 130, 384), (16, 256, 1024), (17, 100, 2560), (63, 513, 640),
+            (64, 1024, 768), (129, 257, 896), (256, 4096, 6144), (200, 2000, 128), (1000, 1032, 1920),
+            (3000, 4096, 512), (2048, 6144, 256), (3333, 4104, 384), (65, 129, 19_584)]
+
+
+@pytest.mark.parametrize("M, N, K", PRODUCTS)
+@pytest.mark.parametrize("e8m0", [False, True])
+@pytest.mark.parametrize("block", [1, 128])
+def test_matmul_whole_numbers_are_exact(eng, M, N, K, e8m0, block):
+    """|terms| <= 9 * 16 and their sums stay below 2^24 quarter-units: every partial sum is exact."""
+    g = gen(M + N + K)
+    a, sa = operand(g, M, K, e8m0, 1, whole=True)
+    b, sb = operand(g, N, K, e8m0, block, whole=True)
+    out = product(eng, a, sa, b, sb, torch.full((M, N), 9.0, device=DEV))
+    ref = deq(a, sa) @ deq(b, sb, block).t()
+    if 9 * 16 * 16 * K < 2 ** 24:  # in units of 2^-4
+        assert torch.equal(out.double(), ref)
+    else:
+        # typical sums are far smaller than the bound on their terms; still exact to fp32
+        assert float((out.double() - ref).abs().max()) <= 2.0 ** -4
+    half = product(eng, a, sa, b, sb, torch.empty((M, N), dtype=BF16, device=DEV))
+    assert same_bits(half, out.to(BF16))
+
+
+@pytest.mark.parametrize("M, N, K", PRODUCTS)
+@pytest.mark.parametrize("e8m0", [False, True])
+@pytest.mark.parametrize("block", [1, 128])
+def test_matmul(eng, M, N, K, e8m0, block):
+    g = gen(M * 3 + N + K)
+    a, sa = operand(g, M, K, e8m0, 1)
+    b, sb = operand(g, N, K, e8m0, block)
+    da, db = deq(a, sa), deq(b, sb, block)
+    ref, mag = da @ db.t(), da.abs() @ db.abs().t()
+    out = product(eng, a, sa, b, sb, torch.full((M, N), 9.0, device=DEV))
+    # a term passes K additions of its own in the worst order; the average is far below
+    assert bool(((out.double() - ref).abs() <= (K + 8) * 2.0 ** -23 * mag).all())
+    assert float((out.double() - ref).norm() / ref.norm()) <= math.sqrt(K) * 2.0 ** -23
+    half = product(eng, a, sa, b, sb, torch.empty((M, N), dtype=BF16, device=DEV))
+    tol = 2.0 ** -8 * ref.abs() + (2.0 ** -12 + (K // 128 + 8) * 2.0 ** -23) * 1.01 * mag
+    assert bool(((half.double() - ref).abs() <= tol).all())
+    assert float((half.double() - ref).norm() / ref.norm()) <= 2.0 ** -8
+
+
+def test_matmul_strided_operands_and_output(eng):
+    g = gen(11)
+    for M, N in ((40, 72), (700, 900)):
+        a, sa = operand(g, M, 512, False, 1)
+        b, sb = operand(g, N, 512, False, 128)
+        wa = torch.zeros((M, 640), dtype=torch.float8_e4m3fn, device=DEV)
+        wb = torch.zeros((N, 528), dtype=torch.float8_e4m3fn, device=DEV)
+        wa[:, 64:576], wb[:, 16:528] = a, b
+        out, untouched = guarded(M, N, F32)
+        work = torch.empty(eng.engram_fp8_matmul_workspace(M, N, 512), dtype=torch.uint8, device=DEV)
+        eng.engram_fp8_matmul(wa[:, 64:576], sa, wb[:, 16:528], sb, out, workspace=work)
+        assert torch.equal(out, product(eng, a, sa, b, sb, torch.empty((M, N), device=DEV))) and untouched()
+
+
+def test_matmul_nan_stays_in_its_row(eng):
+    g = gen(12)
+    for M, N in ((5, 300), (600, 700)):
+        a, sa = operand(g, M, 256, False, 1)
+        b, sb = operand(g, N, 256, False, 128)
+        av = a.view(torch.uint8).clone()
+        av[3, 200] = 0x7F
+        out = product(eng, av, sa, b, sb, torch.empty((M, N), device=DEV))
+        nan = out.isnan()
+        assert bool(nan[3].all()) and int(nan.sum()) == N
+
+
+def test_matmul_of_no_rows(eng):
+    a, sa = operand(gen(1), 4, 128, False, 1)
+    out = torch.empty((0, 4), device=DEV)
+    eng.engram_fp8_matmul(a[:0], sa[:, :0].contiguous(), a, sa, out)
+
+
+def test_matmul_refuses_a_small_workspace(eng):
+    g = gen(13)
+    a, sa = operand(g, 16, 6144, False, 1)
+    b, sb = operand(g, 4096, 6144, False, 128)
+    with pytest.raises(eng.EngramError):
+        eng.engram_fp8_matmul(a, sa, b, sb, torch.empty((16, 4096), device=DEV))
+    with pytest.raises(ValueError):
+        eng.engram_fp8_matmul(a, sa[:, :3].contiguous(), b, sb, torch.empty((16, 4096), device=DEV))
+
+
+# ---------------------------------------------------------------------------
+# gate
+# ---------------------------------------------------------------------------
+
+def gate_forward64(x, v, keep):
+    root = math.sqrt(x.shape[2])
+    z = (x * v[:, None, :]).sum(2, keepdim=True) / root
+    return x + keep[:, None, None] * torch.sigmoid(z) * v[:, None, :]
+
+
+def gate_backward64(x, v, dy, keep):
+    """The formula's gradients and bounds on how far fp32 may be off before the last rounding."""
+    h = x.shape[2]
+    r = 1.0 / math.sqrt(h)
+    vv, k = v[:, None, :], keep[:, None, None]
+    z, za = (x * vv).sum(2, keepdim=True) * r, (x * vv).abs().sum(2, keepdim=True) * r
+    d, da = (dy * vv).sum(2, keepdim=True), (dy * vv).abs().sum(2, keepdim=True)
+    g = torch.sigmoid(z)
+    e = k * d * g * (1 - g) * r
+    dx = dy + e * vv
+    dv = (k * g * dy + e * x).sum(1)
+    # z is off by (h + 2) roundings, the exponentials by a few: 8 covers them and the divisions
+    dz = (h + 2) * E24 * za
+    off_g = 0.25 * dz + 8 * E24
+    off_e = k * r * ((h + 2) * E24 * da * g * (1 - g) + d.abs() * (0.0963 * dz + 16 * E24 * g * (1 - g)))
+    off_dx = off_e * vv.abs() + 2 * E24 * (dy.abs() + (e * vv).abs())
+    off_dv = (k * off_g * dy.abs() + off_e * x.abs() + 6 * E24 * ((k * g * dy).abs() + (e * x).abs())).sum(1)
+    return dx, dv, off_dx, off_dv
+
+
+@pytest.mark.parametrize("T, hidden", [(1, 8), (3, 64), (2, 512), (5, 520), (4, 1024), (33, 2048), (7, 2056), (300, 4096),
+                                       (3, 4104), (2, 8192), (3, 8184)])
+@pytest.mark.parametrize("size", [1.0, 12.0])
+def test_gate_backward(eng, T, hidden, size):
+    g = gen(T + hidden)
+    v, x = randn(g, T, hidden, std=size), randn(g, T, 4, hidden, dtype=BF16)
+    dy = randn(g, T, 4, hidden, dtype=BF16, std=1e-2)
+    keep = (torch.rand(T, generator=g, device=DEV) > 0.3).to(torch.uint8)
+    for mask in (None, keep):
+        dx, dv = torch.empty_like(dy), torch.full((T, hidden), 9.0, device=DEV)
+        eng.engram_gate_add_backward(v, x, dy, dx, dv, keep=mask)
+        k = torch.ones(T, dtype=torch.float64, device=DEV) if mask is None else mask.double()
+        rx, rv, ox, ov = gate_backward64(x.double(), v.double(), dy.double(), k)
+        assert bool(((dx.double() - rx).abs() <= ox + HALF[BF16] * (rx.abs() + ox)).all())
+        assert bool(((dv.double() - rv).abs() <= ov + HALF[F32] * rv.abs() + 1e-40).all())
+        dead = k == 0
+        assert same_bits(dx[dead], dy[dead]) and bool((dv[dead] == 0).all())
+        inplace, dv2 = dy.clone(), torch.empty_like(dv)
+        eng.engram_gate_add_backward(v, x, inplace, inplace, dv2, keep=mask)
+        assert same_bits(inplace, dx) and same_bits(dv2, dv)
+
+
+def test_gate_backward_against_differences(eng):
+    """Central differences of the forward's definition in 64 bits, along random directions."""
+    g = gen(21)
+    T, h = 6, 128
+    v, x, dy = randn(g, T, h), randn(g, T, 4, h, dtype=BF16), randn(g, T, 4, h, dtype=BF16)
+    keep = torch.tensor([1, 0, 1, 1, 1, 1], dtype=torch.uint8, device=DEV)
+    dx, dv = torch.empty_like(dy), torch.empty_like(v)
+    eng.engram_gate_add_backward(v, x, dy, dx, dv, keep=keep)
+    X, V, DY, K = x.double(), v.double(), dy.double(), keep.double()
+    for _ in range(4):
+        ux, uv = torch.randn(X.shape, generator=g, device=DEV).double(), torch.randn(V.shape, generator=g, device=DEV).double()
+        t = 1e-5
+        for ax, av, got, mag in ((ux, 0 * uv, (dx.double() * ux).sum(), (dx.double() * ux).abs().sum()),
+                                 (0 * ux, uv, (dv.double() * uv).sum(), (dv.double() * uv).abs().sum())):
+            up_, down = ((gate_forward64(X + s * t * ax, V + s * t * av, K) * DY).sum() for s in (1.0, -1.0))
+            # half a bf16 step on every dx, 1e-5 of the terms for fp32 and for the difference itself
+            assert abs(float((up_ - down) / (2 * t) - got)) <= (2.0 ** -8 + 1e-5) * float(mag)
+
+
+def test_gate_backward_saturated_gates(eng):
+    """z far out on both sides: no infinity, no NaN, and the small side keeps its relative size."""
+    h = 64
+    v = torch.full((2, h), 8.0, device=DEV)
+    v[1] = -8.0
+    x = torch.full((2, 4, h), 30.0, dtype=BF16, device=DEV)
+    dy = torch.ones((2, 4, h), dtype=BF16, device=DEV)
+    dx, dv = torch.empty_like(dy), torch.empty_like(v)
+    eng.engram_gate_add_backward(v, x, dy, dx, dv)
+    k = torch.ones(2, dtype=torch.float64, device=DEV)
+    rx, rv, ox, ov = gate_backward64(x.double(), v.double(), dy.double(), k)
+    assert bool(torch.isfinite(dx.float()).all()) and bool(torch.isfinite(dv).all())
+    assert bool(((dx.double() - rx).abs() <= ox + HALF[BF16] * (rx.abs() + ox)).all())
+    assert bool(((dv.double() - rv).abs() <= ov + HALF[F32] * rv.abs() + 1e-40).all())
+
+
+# ---------------------------------------------------------------------------
+# streams and graphs
+# ---------------------------------------------------------------------------
+
+def test_operators_on_another_stream_and_in_a_graph(eng):
+    """Every operator captured once and replayed with new inputs between the replays, each replay
+    compared with the same calls made eagerly."""
+    g = gen(31)
+    T, cols, dim, rows, N = 260, 3, 256, 500, 512
+    K = cols * dim
+    table, ids = randn(g, rows, dim), torch.zeros((T, cols), dtype=torch.int32, device=DEV)
+    w = randn(g, N, K, std=0.05)
+    wq, ws = torch.empty((N, K), dtype=torch.float8_e4m3fn, device=DEV), torch.empty((K // 128, N // 128), device=DEV)
+    x, dy = randn(g, T, 4, N, dtype=BF16), randn(g, T, 4, N, dtype=BF16)
+    eng.engram_fp8_quantize(w, wq, ws, block_rows=128)
+    need = max(eng.engram_embed_grad_workspace(T * cols, rows, dim), eng.engram_fp8_matmul_workspace(T, N, K))
+    work = torch.empty(need, dtype=torch.uint8, device=DEV)
+
+    def buffers():
+        return dict(out=torch.empty((T, K), dtype=BF16, device=DEV), q=torch.empty((T, K), dtype=torch.uint8, device=DEV),
+                    s=torch.empty((K // 128, T), device=DEV), v=torch.empty((T, N), device=DEV), dx=torch.empty_like(dy),
+                    dv=torch.empty((T, N), device=DEV), grad=torch.empty((rows, dim), device=DEV),
+                    sgrad=torch.zeros((T * cols, dim), device=DEV), u=torch.empty(T * cols, dtype=torch.int32, device=DEV),
+                    c=torch.empty(1, dtype=torch.int32, device=DEV))
+
+    def step(b, stream=None):
+        eng.engram_embed(table, ids, b["out"], stream=stream)
+        eng.engram_fp8_quantize(b["out"], b["q"], b["s"], stream=stream)
+        eng.engram_fp8_matmul(b["q"], b["s"], wq, ws, b["v"], workspace=work, stream=stream)
+        eng.engram_gate_add_backward(b["v"], x, dy, b["dx"], b["dv"], stream=stream)
+        eng.engram_embed_grad(ids, b["out"], b["grad"], rows=rows, workspace=work, stream=stream)
+        eng.engram_embed_grad(ids, b["out"], b["sgrad"], rows=rows, mode="sparse", unique=b["u"], count=b["c"],
+                              workspace=work, stream=stream)
+
+    eager, replayed = buffers(), buffers()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    step(replayed, side)  # given a stream that is not the current one
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(replayed)
+    for seed in range(4):
+        h = gen(100 + seed)
+        ids.copy_(torch.randint(-1, rows, (T, cols), generator=h, device=DEV, dtype=torch.int32))
+        table.copy_(randn(h, rows, dim))
+        replayed["sgrad"].zero_()
+        eager["sgrad"].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        step(eager)
+        for k in eager:
+            assert same_bits(eager[k], replayed[k]), (seed, k)
