@@ -176,46 +176,61 @@ __device__ __forceinline__ void gemm_fp8_tile(const GemmFp8KArgs& a) {
     const uint32_t* sc = reinterpret_cast<const uint32_t*>(st + SCALES);
     const uint32_t* sca = sc + wm * WM + lrow;
     const uint32_t* scb = sc + BM + wn * WN;
-    i32x8 fb[TN];
+    // The columns' fragments stay in registers for the stage; the rows' are fetched one 16-row
+    // tile ahead of the products.  The scheduling barriers keep the compiler from fetching
+    // every tile at once, which spills.
+    i32x8 fb[WIDE ? 1 : TN];
     bf16x8 wb[WIDE ? TN : 1][4];
     uint32_t sb1[TN];
     f32x4 sb4[TN];
-    float sbw = 1.0f;
+    i32x8 fa = fragment(st, wm * WM + lrow);
+    uint32_t sa = sca[0];
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      fb[j] = fragment(st + A_BYTES, wn * WN + j * 16 + lrow);
+      const i32x8 f = fragment(st + A_BYTES, wn * WN + j * 16 + lrow);
       if (E8M0) sb1[j] = scb[j * 16 + lrow];
       else if (B_ROWS) sb4[j] = *reinterpret_cast<const f32x4*>(scb + j * 16 + 4 * lk);
-      if (WIDE) widen_codes(fb[j], E8M0 ? e8m0_value(sb1[j]) : 1.0f, wb[j]);
+      if (WIDE) widen_codes(f, E8M0 ? e8m0_value(sb1[j]) : 1.0f, wb[j]);
+      else fb[j] = f;
     }
-    if (!E8M0 && !B_ROWS) sbw = __uint_as_float(scb[0]);
+    const float sbw = !E8M0 && !B_ROWS ? __uint_as_float(scb[0]) : 1.0f;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      const i32x8 fa = fragment(st, wm * WM + i * 16 + lrow);
-      const uint32_t sa = sca[i * 16];
+      __builtin_amdgcn_sched_barrier(0);
       bf16x8 wa[4];
       if (WIDE) widen_codes(fa, E8M0 ? e8m0_value(sa) : 1.0f, wa);
+      const i32x8 f = fa;
+      const uint32_t s1 = sa;
+      if (i + 1 < TM) {
+        fa = fragment(st, wm * WM + (i + 1) * 16 + lrow);
+        sa = sca[(i + 1) * 16];
+      }
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        if (WIDE && E8M0) {
+        if (E8M0) {
+          if (WIDE) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][q], wa[q], acc[i][j], 0, 0, 0);
-        } else if (E8M0) {
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa, acc[i][j], 0, 0, 0, (int)sb1[j], 0,
-                                                                       (int)sa);
+            for (int q = 0; q < 4; ++q)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][q], wa[q], acc[i][j], 0, 0, 0);
+          } else {
+            acc[i][j] =
+                __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], f, acc[i][j], 0, 0, 0, (int)sb1[j], 0, (int)s1);
+          }
         } else {
           f32x4 p = {};
           if (WIDE) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][q], wa[q], p, 0, 0, 0);
           } else {
-            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa, p, 0, 0, 0, 0, 0, 0);
+            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], f, p, 0, 0, 0, 0, 0, 0);
           }
-          const float s = __uint_as_float(sa) * sbw;
+          const float s = __uint_as_float(s1) * sbw;
 #pragma unroll
           for (int v = 0; v < 4; ++v)
-            acc[i][j][v] = fmaf(p[v], B_ROWS ? __uint_as_float(sa) * sb4[j][v] : s, acc[i][j][v]);
+            acc[i][j][v] = fmaf(p[v], B_ROWS ? __uint_as_float(s1) * sb4[j][v] : s, acc[i][j][v]);
+          // keeps the fold here: moved behind all products, as the compiler would, it holds
+          // every product's registers at once
+          asm volatile("" : "+v"(acc[i][j]));
         }
       }
     }
