@@ -18,12 +18,12 @@
 // lines, XOR-swizzled chunks).
 //
 // The operands are swapped (B is the first), so a lane's four results are four consecutive n
-// of one m: its scale of A is one value, and C is stored in 16-byte pieces.
+// of one m, and its scale of A is one value.
 //
 // Scales.  e8m0 bytes go into the 8-bit instruction, or into the widening, and the products
 // accumulate in place.  fp32 scales cannot: the block's product starts from zero and one fma per
 // result folds it into the accumulator with sa sb; with a 128 x 128 scale of B that factor is
-// one value per 16 rows for the whole wave, with one scale per row of B a vector of four.
+// one value per lane and row tile, with one scale per row of B a vector of four.
 // A stage's scales are staged in LDS beside its operands: thread t of the workgroup (as many
 // threads as rows of A and B) loads entry t.
 
@@ -55,7 +55,7 @@ __device__ __forceinline__ void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// 32 codes to bf16, times 2^(byte - 127): the operands of four k32 steps
+// 32 codes to bf16, times a power of two: the operands of four k32 steps
 __device__ __forceinline__ void widen_codes(const i32x8& q, float scale, bf16x8* o) {
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
@@ -99,7 +99,7 @@ __device__ __forceinline__ void gemm_fp8_tile(const GemmFp8KArgs& a) {
   const int kb0 = split * a.kb_per_split;
   const int nk = min(a.kb_per_split, a.KB - kb0);
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN_WAVES, wn = wave % WN_WAVES;
   const int rows_a = min(a.M - m0, BM), rows_b = min(a.N - n0, BN);
   const __amdgpu_buffer_rsrc_t arsrc = __builtin_amdgcn_make_buffer_rsrc(
@@ -109,48 +109,39 @@ __device__ __forceinline__ void gemm_fp8_tile(const GemmFp8KArgs& a) {
 
   // direct loads: wave w, load i fills LDS bytes [(NWAVES i + w) KB, +1 KB) of the operand;
   // 8 lanes fetch one row's 128 bytes.  Rows past the matrix read its last row (never stored).
-  int aoff[AI], boff[BI];
+  int offset[AI + BI];
 #pragma unroll
-  for (int i = 0; i < AI; ++i) {
-    const int P = 64 * (i * NWAVES + wave) + lane, row = P >> 3, c = (P & 7) ^ gemm_swz(row);
-    aoff[i] = min(row, rows_a - 1) * (int)a.lda + 16 * c;
+  for (int i = 0; i < AI + BI; ++i) {
+    const bool of_a = i < AI;
+    const int row = ((of_a ? i : i - AI) * NWAVES + wave) * 8 + (lane >> 3), c = (lane & 7) ^ gemm_swz(row);
+    offset[i] = min(row, (of_a ? rows_a : rows_b) - 1) * (int)(of_a ? a.lda : a.ldb) + 16 * c;
   }
-#pragma unroll
-  for (int i = 0; i < BI; ++i) {
-    const int P = 64 * (i * NWAVES + wave) + lane, row = P >> 3, c = (P & 7) ^ gemm_swz(row);
-    boff[i] = min(row, rows_b - 1) * (int)a.ldb + 16 * c;
-  }
-  auto issue = [&](int kt) {
-    char* st = smem + (kt & 1) * STAGE;
-    const int k = (kb0 + kt) * 128;
-#pragma unroll
-    for (int i = 0; i < AI; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(arsrc, (ENGRAM_LDS_AS void*)(st + (i * NWAVES + wave) * 1024), 16,
-                                               aoff[i] + k, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < BI; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(brsrc, (ENGRAM_LDS_AS void*)(st + A_BYTES + (i * NWAVES + wave) * 1024),
-                                               16, boff[i] + k, 0, 0, 0);
+  // load i of stage kt; stages past the end: the last one again, into a slot nobody reads
+  auto issue = [&](int kt, int i) {
+    const int k = (kb0 + min(kt, nk - 1)) * 128;
+    const int to = (kt & 1) * STAGE + (i < AI ? i : i - AI) * NWAVES * 1024 + (i < AI ? 0 : A_BYTES) + wave * 1024;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(i < AI ? arsrc : brsrc, (ENGRAM_LDS_AS void*)(smem + to), 16, offset[i], k, 0,
+                                             0);
   };
   // the thread's scale entry: rows of A first, then rows (or 128-blocks) of B
-  const bool is_a = tid < BM;
+  const bool is_a = wave * 64 < BM;
   const int64_t s_ld = is_a ? a.M : a.sb_ld;
-  const int64_t s_at = is_a ? m0 + min(tid, rows_a - 1) : (n0 + min(tid - BM, rows_b - 1)) >> a.b_shift;
-  const void* s_base = is_a ? a.sa : a.sb;
+  const char* s_base = static_cast<const char*>(is_a ? a.sa : a.sb) + (int64_t)kb0 * s_ld * (E8M0 ? 1 : 4);
+  const int s_at = is_a ? m0 + min(tid, rows_a - 1) : (n0 + min(tid - BM, rows_b - 1)) >> a.b_shift;
   auto load_scale = [&](int kt) -> uint32_t {
-    const int64_t e = (int64_t)(kb0 + kt) * s_ld + s_at;
-    return E8M0 ? (uint32_t) static_cast<const uint8_t*>(s_base)[e] : static_cast<const uint32_t*>(s_base)[e];
+    const char* p = s_base + min(kt, nk - 1) * s_ld * (E8M0 ? 1 : 4);
+    return E8M0 ? (uint32_t)reinterpret_cast<const uint8_t*>(p)[s_at] : reinterpret_cast<const uint32_t*>(p)[s_at];
   };
   auto put_scale = [&](int kt, uint32_t s) {
     reinterpret_cast<uint32_t*>(smem + (kt & 1) * STAGE + SCALES)[tid] = s;
   };
 
   const int lrow = lane & 15, lk = lane >> 4;
-  auto fragment = [&](const char* base, int row) -> i32x8 {
-    const char* p = base + row * 128;
-    const int z = gemm_swz(row);
-    const i32x4 lo = *reinterpret_cast<const i32x4*>(p + 16 * (lk ^ z));
-    const i32x4 hi = *reinterpret_cast<const i32x4*>(p + 16 * ((lk + 4) ^ z));
+  // row r0 + l % 16's codes (r0 a multiple of 16, whose rows share the swizzle)
+  const int off0 = lrow * 128 + 16 * (lk ^ gemm_swz(lrow)), off1 = lrow * 128 + 16 * ((lk + 4) ^ gemm_swz(lrow));
+  auto fragment = [&](const char* base, int r0) -> i32x8 {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(base + r0 * 128 + off0);
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(base + r0 * 128 + off1);
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
 
@@ -160,117 +151,149 @@ __device__ __forceinline__ void gemm_fp8_tile(const GemmFp8KArgs& a) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{};
 
+  // fp32 scales: the block product of the tile before the current one, still to be folded
+  // into its accumulator (times its scales) while the current one multiplies
+  f32x4 p_old = {}, s_old = {};
+  auto fold = [&](int i, int j) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(p_old[v], B_ROWS ? s_old[v] : s_old[0], acc[i][j][v]);
+    // keeps the fold here: moved behind all products, as the compiler would, it holds every
+    // product's registers at once
+    asm volatile("" : "+v"(acc[i][j]));
+  };
+
   uint32_t sreg = load_scale(0);
-  issue(0);
+#pragma unroll
+  for (int i = 0; i < AI + BI; ++i) issue(0, i);
   wait_vmcnt<0>();
   put_scale(0, sreg);
   wait_lgkmcnt0();
   stage_barrier();
   for (int kt = 0; kt < nk; ++kt) {
-    const bool more = kt + 1 < nk;
-    if (more) {
-      sreg = load_scale(kt + 1);
-      issue(kt + 1);
-    }
+    // past the end: the last stage again, into a slot nobody reads
+    sreg = load_scale(kt + 1);
     const char* st = smem + (kt & 1) * STAGE;
-    const uint32_t* sc = reinterpret_cast<const uint32_t*>(st + SCALES);
-    const uint32_t* sca = sc + wm * WM + lrow;
-    const uint32_t* scb = sc + BM + wn * WN;
-    // The columns' fragments stay in registers for the stage; the rows' are fetched one 16-row
-    // tile ahead of the products.  The scheduling barriers keep the compiler from fetching
-    // every tile at once, which spills.
-    i32x8 fb[WIDE ? 1 : TN];
+    const char* sta = st + wm * WM * 128;
+    const char* stb = st + A_BYTES + wn * WN * 128;
+    const uint32_t* sca = reinterpret_cast<const uint32_t*>(st + SCALES) + wm * WM + lrow;
+    const uint32_t* scb = reinterpret_cast<const uint32_t*>(st + SCALES) + BM + wn * WN;
+    i32x8 fb[TN];
     bf16x8 wb[WIDE ? TN : 1][4];
     uint32_t sb1[TN];
-    f32x4 sb4[TN];
-    i32x8 fa = fragment(st, wm * WM + lrow);
-    uint32_t sa = sca[0];
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const i32x8 f = fragment(st + A_BYTES, wn * WN + j * 16 + lrow);
+    f32x4 sb4[TN];  // one scale per row of B: held for the stage, or (WIDE, no registers) read where used
+    auto fetch_b = [&](int j) {
+      fb[j] = fragment(stb, j * 16);
       if (E8M0) sb1[j] = scb[j * 16 + lrow];
-      else if (B_ROWS) sb4[j] = *reinterpret_cast<const f32x4*>(scb + j * 16 + 4 * lk);
-      if (WIDE) widen_codes(f, E8M0 ? e8m0_value(sb1[j]) : 1.0f, wb[j]);
-      else fb[j] = f;
-    }
+      if (!E8M0 && B_ROWS && !WIDE) sb4[j] = *reinterpret_cast<const f32x4*>(scb + j * 16 + 4 * lk);
+    };
+    fetch_b(0);
+    i32x8 fa = fragment(sta, 0);
+    uint32_t sa = sca[0];
     const float sbw = !E8M0 && !B_ROWS ? __uint_as_float(scb[0]) : 1.0f;
+    if (TN > 1) fetch_b(1);
+    if (WIDE) widen_codes(fb[0], E8M0 ? e8m0_value(sb1[0]) : 1.0f, wb[0]);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      __builtin_amdgcn_sched_barrier(0);
+      // Of the two waves of a SIMD the one that is behind goes first: left to their age, the
+      // older four run ahead, wait at the barrier for a third of the stage, and each wave
+      // alone cannot keep the matrix cores fed.  (Tiles of 128 run two or three workgroups
+      // per CU, and were up to 15% slower with it.)
+      if (BM == 256 && i % (TM / 4) == 0) {
+        if (i * 4 / TM == 0) __builtin_amdgcn_s_setprio(3);
+        if (i * 4 / TM == 1) __builtin_amdgcn_s_setprio(2);
+        if (i * 4 / TM == 2) __builtin_amdgcn_s_setprio(1);
+        if (i * 4 / TM == 3) __builtin_amdgcn_s_setprio(0);
+      }
+      // the next stage's loads, spread over the first row tiles: issued at once they held the
+      // wave for up to a thousand of a stage's 5,000 to 8,000 cycles
+      constexpr int PER = (AI + BI + TM / 2 - 1) / (TM / 2);
+#pragma unroll
+      for (int e = 0; e < PER; ++e)
+        if (i * PER + e < AI + BI) issue(kt + 1, i * PER + e);
       bf16x8 wa[4];
       if (WIDE) widen_codes(fa, E8M0 ? e8m0_value(sa) : 1.0f, wa);
       const i32x8 f = fa;
       const uint32_t s1 = sa;
-      if (i + 1 < TM) {
-        fa = fragment(st, wm * WM + (i + 1) * 16 + lrow);
+      if (i + 1 < TM) {  // the next row tile, one ahead of the products
+        fa = fragment(sta, (i + 1) * 16);
         sa = sca[(i + 1) * 16];
       }
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        if (E8M0) {
-          if (WIDE) {
+        // one tile: its products, the fold of the tile before, and in the first row tile the
+        // next columns' operands.  Nothing crosses to another tile: free to, the compiler
+        // fetches and folds everything at once, and spills.
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 p = E8M0 ? acc[i][j] : f32x4{};
+        if (WIDE) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][q], wa[q], acc[i][j], 0, 0, 0);
-          } else {
-            acc[i][j] =
-                __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], f, acc[i][j], 0, 0, 0, (int)sb1[j], 0, (int)s1);
-          }
+          for (int q = 0; q < 4; ++q) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][q], wa[q], p, 0, 0, 0);
+        } else if (E8M0) {
+          p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], f, p, 0, 0, 0, (int)sb1[j], 0, (int)s1);
         } else {
-          f32x4 p = {};
-          if (WIDE) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][q], wa[q], p, 0, 0, 0);
-          } else {
-            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], f, p, 0, 0, 0, 0, 0, 0);
-          }
-          const float s = __uint_as_float(s1) * sbw;
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            acc[i][j][v] = fmaf(p[v], B_ROWS ? __uint_as_float(s1) * sb4[j][v] : s, acc[i][j][v]);
-          // keeps the fold here: moved behind all products, as the compiler would, it holds
-          // every product's registers at once
-          asm volatile("" : "+v"(acc[i][j]));
+          p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], f, p, 0, 0, 0, 0, 0, 0);
+        }
+        if (i == 0 && j + 2 < TN) fetch_b(j + 2);
+        if (WIDE && i == 0 && j + 1 < TN) widen_codes(fb[j + 1], E8M0 ? e8m0_value(sb1[j + 1]) : 1.0f, wb[j + 1]);
+        if (E8M0) {
+          acc[i][j] = p;
+        } else {
+          const int t = i * TN + j + TM * TN - 1;
+          fold(t / TN % TM, t % TN);
+          p_old = p;
+          if (B_ROWS && WIDE) sb4[j] = *reinterpret_cast<const f32x4*>(scb + j * 16 + 4 * lk);
+          if (B_ROWS) s_old = __uint_as_float(s1) * sb4[j];
+          else s_old[0] = __uint_as_float(s1) * sbw;
         }
       }
     }
-    if (more) {
-      wait_vmcnt<0>();
-      put_scale(kt + 1, sreg);
-    }
+    wait_vmcnt<0>();
+    put_scale(kt + 1, sreg);
     wait_lgkmcnt0();
     stage_barrier();
   }
+  if (!E8M0) fold(TM - 1, TN - 1);
 
-  // lane: row m = lrow, columns 4 lk .. +4 of each 16 x 16 tile
+  // C: lane l holds of each 16 x 16 tile row m = l % 16 and columns 4 (l / 16) .. +4.
+  // Each wave lays 16 rows of its columns out in LDS (the ring is done with: the loads of the
+  // stage past the end have landed) and writes them as whole row segments.
+  constexpr int PITCH = WN + 4;
+  static_assert(NWAVES * 16 * PITCH * 4 <= 2 * STAGE, "the slabs fit in the ring");
+  float* slab = reinterpret_cast<float*>(smem) + wave * 16 * PITCH;
   const int64_t base = (int64_t)split * a.c_split_stride;
+  constexpr int LANES = WN / 4, ROWS = 64 / LANES;  // lanes per row, rows per pass
+  const int n = n0 + wn * WN + (lane % LANES) * 4;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int m = m0 + wm * WM + i * 16 + lrow;
-    if (m >= a.M) continue;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int n = n0 + wn * WN + j * 16 + 4 * lk;
-      if (n >= a.N) continue;
+    for (int j = 0; j < TN; ++j) *reinterpret_cast<f32x4*>(slab + lrow * PITCH + j * 16 + 4 * lk) = acc[i][j];
+    asm volatile("" ::: "memory");  // a wave's own LDS accesses keep their order
+#pragma unroll
+    for (int q = 0; q < 16 / ROWS; ++q) {
+      const int r = q * ROWS + lane / LANES;
+      const f32x4 val = *reinterpret_cast<const f32x4*>(slab + r * PITCH + (lane % LANES) * 4);
+      const int m = m0 + wm * WM + i * 16 + r;
+      if (m >= a.M || n >= a.N) continue;
       const int64_t at = base + (int64_t)m * a.ldc + n;
       if (a.vec_store && n + 4 <= a.N) {
         if (a.c_f32) {
-          *reinterpret_cast<f32x4*>(static_cast<float*>(a.C) + at) = acc[i][j];
+          *reinterpret_cast<f32x4*>(static_cast<float*>(a.C) + at) = val;
         } else {
           uint2 o;
-          o.x = bf16_bits_rne(acc[i][j][0]) | (bf16_bits_rne(acc[i][j][1]) << 16);
-          o.y = bf16_bits_rne(acc[i][j][2]) | (bf16_bits_rne(acc[i][j][3]) << 16);
+          o.x = bf16_bits_rne(val[0]) | (bf16_bits_rne(val[1]) << 16);
+          o.y = bf16_bits_rne(val[2]) | (bf16_bits_rne(val[3]) << 16);
           *reinterpret_cast<uint2*>(static_cast<unsigned short*>(a.C) + at) = o;
         }
       } else {
 #pragma unroll
         for (int v = 0; v < 4; ++v)
           if (n + v < a.N) {
-            if (a.c_f32) static_cast<float*>(a.C)[at + v] = acc[i][j][v];
-            else static_cast<unsigned short*>(a.C)[at + v] = (unsigned short)bf16_bits_rne(acc[i][j][v]);
+            if (a.c_f32) static_cast<float*>(a.C)[at + v] = val[v];
+            else static_cast<unsigned short*>(a.C)[at + v] = (unsigned short)bf16_bits_rne(val[v]);
           }
       }
     }
+    asm volatile("" ::: "memory");
   }
 }
 

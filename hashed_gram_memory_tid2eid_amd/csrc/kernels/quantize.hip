@@ -107,7 +107,7 @@ __global__ __launch_bounds__(kQuantThreads) void fp8_quantize_kernel(QuantKArgs 
   }
 
   uint32_t block_max = 0;
-  if (COLS || BLOCK) {
+  if constexpr (COLS || BLOCK) {
     uint32_t cm[8] = {};
 #pragma unroll
     for (int i = 0; i < RT; ++i)
@@ -178,7 +178,7 @@ __global__ __launch_bounds__(kQuantThreads) void fp8_quantize_kernel(QuantKArgs 
     }
   }
 
-  if (COLS) {
+  if constexpr (COLS) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int col = c * 8 + j;
