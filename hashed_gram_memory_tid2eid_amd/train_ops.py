@@ -21,50 +21,74 @@ _SCALES = {torch.float32: ENGRAM_FP8_SCALE_F32, torch.uint8: ENGRAM_FP8_SCALE_E8
 
 
 def _matrix(t, name, types):
-    """(pointer, leading dimension) of a device matrix whose rows are contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if t.dtype not in types:
-        raise TypeError(f"{name} must be one of {[str(x) for x in types]}, got {t.dtype}")
+    """(pointer, rows, columns, leading dimension, type) of a device matrix whose rows are contiguous."""
+    try:
+        kind = types[t.dtype]
+        rows, cols = t.shape
+        ld, step = t.stride()
+    except (AttributeError, KeyError, ValueError):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor") from None
+        if t.dtype not in types:
+            raise TypeError(f"{name} must be one of {[str(x) for x in types]}, got {t.dtype}") from None
+        raise ValueError(f"{name} must be a matrix") from None
     if not t.is_cuda:
         raise TypeError(f"{name} must be a device tensor")
-    _need(t.dim() == 2, f"{name} must be a matrix")
-    _need(t.shape[1] <= 1 or t.stride(1) == 1, f"{name} must have contiguous rows")
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    _need(ld >= t.shape[1], f"{name} must not have overlapping rows")
-    return t.data_ptr(), ld
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:
+        ld = cols
+    elif ld < cols:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return t.data_ptr(), rows, cols, ld, kind
 
 
-def _same_device(*tensors):
-    devices = {t.device for t in tensors if t is not None}
-    _need(len(devices) <= 1, f"tensors on different devices: {sorted(map(str, devices))}")
+def _flat(t, name, dtype):
+    """Pointer of a contiguous device tensor of one type."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        return _dev(t, dtype, name)  # says what is wrong
+    return t.data_ptr()
+
+
+def _launch_stream(stream, *tensors):
+    """The raw stream of a call whose tensors must all live on one device."""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d != dev and dev != -1:
+                raise ValueError(f"tensors on different devices: {dev} and {d}")
+            dev = d
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _work(workspace):
     if workspace is None:
         return None, 0
-    return _dev(workspace, None, "workspace"), workspace.numel() * workspace.element_size()
+    return _flat(workspace, "workspace", workspace.dtype), workspace.numel() * workspace.element_size()
+
+
+_INT = {torch.int32: None}
 
 
 def _ids(ids):
     """(pointer, T, columns, leading dimension) of int32 ids [T] or [T][columns]."""
     m = ids.unsqueeze(1) if isinstance(ids, torch.Tensor) and ids.dim() == 1 else ids
-    p, ld = _matrix(m, "ids", (torch.int32,))
-    _need(m.shape[1] >= 1, "ids need a column")
-    return p, m.shape[0], m.shape[1], ld
+    p, T, cols, ld, _ = _matrix(m, "ids", _INT)
+    _need(cols >= 1, "ids need a column")
+    return p, T, cols, ld
 
 
 def engram_embed(table, ids, out, *, scale=1.0, seg_pitch=None, stream=None):
     """out[t][c * seg_pitch + d] = scale * table[ids[t][c]][d]; ids int32 [T] or [T][columns],
     -1 for none; seg_pitch defaults to the table's width."""
-    tp, table_ld = _matrix(table, "table", _WIDE)
+    tp, rows, dim, table_ld, table_type = _matrix(table, "table", _WIDE)
     ip, T, cols, ids_ld = _ids(ids)
-    op, out_ld = _matrix(out, "out", _WIDE)
-    _same_device(table, ids, out)
-    seg = table.shape[1] if seg_pitch is None else int(seg_pitch)
-    _need(out.shape[0] >= T and out.shape[1] >= cols * seg, "out too small")
-    _check(_lib.engram_embed(tp, _WIDE[table.dtype], table.shape[0], table.shape[1], table_ld, ip, T, cols, ids_ld,
-                             float(scale), op, _WIDE[out.dtype], out_ld, seg, _stream(stream)), "engram_embed")
+    op, out_rows, out_cols, out_ld, out_type = _matrix(out, "out", _WIDE)
+    seg = dim if seg_pitch is None else seg_pitch
+    _need(out_rows >= T and out_cols >= cols * seg, "out too small")
+    _check(_lib.engram_embed(tp, table_type, rows, dim, table_ld, ip, T, cols, ids_ld, scale, op, out_type, out_ld, seg,
+                             _launch_stream(stream, table, ids, out)), "engram_embed")
 
 
 def engram_embed_grad_workspace(places: int, rows: int, dim: int) -> int:
@@ -83,25 +107,24 @@ def engram_embed_grad(ids, dout, grad, *, rows, scale=1.0, mode="dense", seg_pit
     number into ``count``."""
     _need(mode in _GRAD_MODES, f"unknown mode {mode!r}")
     ip, T, cols, ids_ld = _ids(ids)
-    dp, dout_ld = _matrix(dout, "dout", _WIDE)
-    gp, grad_ld = _matrix(grad, "grad", _WIDE)
-    _same_device(ids, dout, grad, unique, count, workspace)
-    dim = grad.shape[1]
-    seg = dim if seg_pitch is None else int(seg_pitch)
-    _need(dout.shape[0] >= T and dout.shape[1] >= cols * seg, "dout too small")
-    _need(grad.shape[0] >= (T * cols if mode == "sparse" else rows), "grad has too few rows")
+    dp, dout_rows, dout_cols, dout_ld, dout_type = _matrix(dout, "dout", _WIDE)
+    gp, grad_rows, dim, grad_ld, grad_type = _matrix(grad, "grad", _WIDE)
+    seg = dim if seg_pitch is None else seg_pitch
+    _need(dout_rows >= T and dout_cols >= cols * seg, "dout too small")
+    _need(grad_rows >= (T * cols if mode == "sparse" else rows), "grad has too few rows")
     up = cp = None
     if mode == "sparse":
         _need(unique is not None and count is not None, "a sparse gradient needs unique and count")
+        up, cp = _flat(unique, "unique", torch.int32), _flat(count, "count", torch.int32)
         _need(unique.numel() >= T * cols and count.numel() >= 1, "unique / count too small")
-        up, cp = _dev(unique, torch.int32, "unique"), _dev(count, torch.int32, "count")
     wp, wn = _work(workspace)
-    _check(_lib.engram_embed_grad(ip, T, cols, ids_ld, int(rows), dim, float(scale), dp, _WIDE[dout.dtype], dout_ld, seg,
-                                  _GRAD_MODES[mode], gp, _WIDE[grad.dtype], grad_ld, up, cp, wp, wn, _stream(stream)),
+    _check(_lib.engram_embed_grad(ip, T, cols, ids_ld, rows, dim, scale, dp, dout_type, dout_ld, seg, _GRAD_MODES[mode],
+                                  gp, grad_type, grad_ld, up, cp, wp, wn,
+                                  _launch_stream(stream, ids, dout, grad, unique, count, workspace)),
            "engram_embed_grad")
 
 
-_CODES = (torch.float8_e4m3fn, torch.uint8)
+_CODES = {torch.float8_e4m3fn: None, torch.uint8: None}
 
 
 def _blocks(n):
@@ -114,13 +137,15 @@ def _codes_and_scales(q, scales, n, k, block, name):
         _need(scales is None, f"{name} scales without codes")
         return None, 0, None, None
     _need(scales is not None, f"{name} codes need scales")
-    p, ld = _matrix(q, name, _CODES)
-    _need(q.shape[0] >= n and q.shape[1] >= 128 * _blocks(k), f"{name} codes too small")
-    if scales.dtype not in _SCALES:
+    p, rows, cols, ld, _ = _matrix(q, name, _CODES)
+    kb = _blocks(k)
+    _need(rows >= n and cols >= 128 * kb, f"{name} codes too small")
+    kind = _SCALES.get(scales.dtype)
+    if kind is None:
         raise TypeError(f"{name} scales must be float32, or uint8 (e8m0)")
-    want = (_blocks(k), n if block == 1 else _blocks(n))
-    _need(tuple(scales.shape) == want, f"{name} scales must be {list(want)}, got {list(scales.shape)}")
-    return p, ld, _dev(scales, None, f"{name} scales"), _SCALES[scales.dtype]
+    if scales.shape != (kb, n if block == 1 else _blocks(n)):
+        raise ValueError(f"{name} scales must be {[kb, n if block == 1 else _blocks(n)]}, got {list(scales.shape)}")
+    return p, ld, _flat(scales, f"{name} scales", scales.dtype), kind
 
 
 def engram_fp8_quantize(x, q, scales, *, q_t=None, scales_t=None, block_rows=1, stream=None):
@@ -128,15 +153,14 @@ def engram_fp8_quantize(x, q, scales, *, q_t=None, scales_t=None, block_rows=1, 
     the transpose q_t [K][M up to 128s] with scales_t [M/128][K]; block_rows=128 takes one scale
     per 128 x 128 (scales [K/128][M/128])."""
     _need(block_rows in (1, 128), "block_rows must be 1 or 128")
-    xp, x_ld = _matrix(x, "x", _WIDE)
-    M, K = x.shape
+    xp, M, K, x_ld, x_type = _matrix(x, "x", _WIDE)
     _need(q is not None or q_t is not None, "no output: give q or q_t")
     qp, q_ld, sp, kind = _codes_and_scales(q, scales, M, K, block_rows, "q")
     tp, t_ld, stp, kind_t = _codes_and_scales(q_t, scales_t, K, M, block_rows, "q_t")
     _need(kind is None or kind_t is None or kind == kind_t, "both scales must be of one type")
-    _same_device(x, q, scales, q_t, scales_t)
-    _check(_lib.engram_fp8_quantize(xp, _WIDE[x.dtype], M, K, x_ld, kind if kind is not None else kind_t, block_rows, qp,
-                                    q_ld, sp, tp, t_ld, stp, _stream(stream)), "engram_fp8_quantize")
+    _check(_lib.engram_fp8_quantize(xp, x_type, M, K, x_ld, kind if kind is not None else kind_t, block_rows, qp, q_ld, sp,
+                                    tp, t_ld, stp, _launch_stream(stream, x, q, scales, q_t, scales_t)),
+           "engram_fp8_quantize")
 
 
 def engram_fp8_matmul_workspace(M: int, N: int, K: int) -> int:
@@ -150,37 +174,38 @@ def engram_fp8_matmul_workspace(M: int, N: int, K: int) -> int:
 def engram_fp8_matmul(a, scales_a, b, scales_b, out, *, workspace=None, stream=None):
     """out[m][n] = sum_k a[m][k] b[n][k] of quantised operands: a [M][K] with scales [K/128][M],
     b [N][K] with scales [K/128][N] or [K/128][N/128]; K whole blocks of 128."""
-    op, out_ld = _matrix(out, "out", _WIDE)
-    M, N = out.shape
+    op, M, N, out_ld, out_type = _matrix(out, "out", _WIDE)
     _need(isinstance(a, torch.Tensor) and isinstance(b, torch.Tensor) and a.dim() == 2 and b.dim() == 2,
           "a and b must be matrices")
-    K = a.shape[1]
-    _need(K % 128 == 0 and K > 0 and b.shape[1] == K, "a and b need the same K, whole blocks of 128")
-    _need(a.shape[0] == M and b.shape[0] == N, "out must be [rows of a][rows of b]")
+    (rows_a, K), (rows_b, kb) = a.shape, b.shape
+    _need(K % 128 == 0 and K > 0 and kb == K, "a and b need the same K, whole blocks of 128")
+    _need(rows_a == M and rows_b == N, "out must be [rows of a][rows of b]")
     block = 1 if scales_b.dim() == 2 and scales_b.shape[1] == N else 128
     ap, a_ld, sap, kind = _codes_and_scales(a, scales_a, M, K, 1, "a")
     bp, b_ld, sbp, kind_b = _codes_and_scales(b, scales_b, N, K, block, "b")
     _need(kind == kind_b, "both scales must be of one type")
-    _same_device(a, scales_a, b, scales_b, out, workspace)
     wp, wn = _work(workspace)
-    _check(_lib.engram_fp8_matmul(ap, a_ld, sap, bp, b_ld, sbp, block, kind, M, N, K, op, _WIDE[out.dtype], out_ld, wp, wn,
-                                  _stream(stream)), "engram_fp8_matmul")
+    _check(_lib.engram_fp8_matmul(ap, a_ld, sap, bp, b_ld, sbp, block, kind, M, N, K, op, out_type, out_ld, wp, wn,
+                                  _launch_stream(stream, a, scales_a, b, scales_b, out, workspace)), "engram_fp8_matmul")
 
 
 def engram_gate_add_backward(v, streams, dy, dx, dv, *, keep=None, T=None, stream=None):
     """Gradients of engram_gate_add: dx of the streams [T][hc][hidden] before the add (dx may be
     dy) and dv of v, from the streams before the add and dy of the streams after it."""
+    _need(streams.dim() == 3, "streams must be [T][hc][hidden]")
+    n, hc, hidden = streams.shape
     if T is None:
-        T = streams.shape[0]
-    _need(streams.dim() == 3 and streams.shape[0] >= T, "streams must be [T][hc][hidden]")
-    hc, hidden = streams.shape[1], streams.shape[2]
+        T = n
+    _need(n >= T, "streams must be [T][hc][hidden]")
     for t, name in ((dy, "dy"), (dx, "dx")):
-        _need(t.dim() == 3 and t.shape[0] >= T and t.shape[1:] == streams.shape[1:], f"{name} must be [T][hc][hidden]")
+        shape = t.shape
+        _need(len(shape) == 3 and shape[0] >= T and shape[1] == hc and shape[2] == hidden, f"{name} must be [T][hc][hidden]")
     for t, name in ((v, "v"), (dv, "dv")):
-        _need(t.dim() == 2 and t.shape[0] >= T and t.shape[1] == hidden, f"{name} must be [T][hidden]")
+        shape = t.shape
+        _need(len(shape) == 2 and shape[0] >= T and shape[1] == hidden, f"{name} must be [T][hidden]")
     _need(keep is None or keep.numel() >= T, "keep too small")
-    _same_device(v, streams, dy, dx, dv, keep)
     _check(_lib.engram_gate_add_backward(
-        _dev(v, torch.float32, "v"), _dev(streams, torch.bfloat16, "streams"), _dev(keep, torch.uint8, "keep"),
-        _dev(dy, torch.bfloat16, "dy"), hidden, hc, _dev(dx, torch.bfloat16, "dx"), _dev(dv, torch.float32, "dv"), T,
-        _stream(stream)), "engram_gate_add_backward")
+        _flat(v, "v", torch.float32), _flat(streams, "streams", torch.bfloat16),
+        None if keep is None else _flat(keep, "keep", torch.uint8), _flat(dy, "dy", torch.bfloat16), hidden, hc,
+        _flat(dx, "dx", torch.bfloat16), _flat(dv, "dv", torch.float32), T,
+        _launch_stream(stream, v, streams, dy, dx, dv, keep)), "engram_gate_add_backward")
