@@ -3,22 +3,30 @@
 //
 //   grad[r][d] = scale * sum over the places (t, c) with ids[t][c] = r of dout[t][c seg_pitch + d]
 //
-// The places are sorted by row id (a stable radix sort, 8 bits a pass, over as many bits as
-// the table's row count has; id -1 and ids outside the table sort behind every row), so a
-// row's places are one run.  The sorted list is cut into chunks of `ch` places; a group of
-// lanes owns one chunk and one range of columns, 8 per lane, and walks it with fp32 sums in
-// registers.  A run inside a chunk is finished there and written once.  Runs that cross
-// chunks leave partial rows: `head` (a run that came in from the chunk before) and `tail` (a
-// run that starts here and goes on); a second level joins kJoin chunks the same way, and the
-// last kernel joins what crosses those.  Nothing is added by atomics: the order of every sum
-// follows the sorted places, so results repeat bit for bit.
+// The places are sorted by row id (a stable radix sort over as many bits as the table's row
+// count has; id -1 and ids outside the table sort behind every row), so a row's places are
+// one run.  Up to kSmallSort places one workgroup sorts them in LDS, in one launch that also
+// clears a dense gradient (its other workgroups write the zeros: at 16,384 places the sort
+// hides behind 2 GB of them); more take three launches for each digit of up to 10 bits.
+//
+// The sorted list is cut into chunks of `ch` places; a group of lanes owns one chunk and one
+// range of columns, 8 per lane, and walks it with fp32 sums in registers.  A run inside a
+// chunk is finished there and written once.  Runs that cross chunks leave partial rows:
+// `head` (a run that came in from the chunk before) and `tail` (a run that starts here and
+// goes on); the group of the chunk where such a run starts adds them up.  So that a row that
+// holds much of the batch is not one long chain, units of kUnit chunks inside one run are
+// added first, each by a group of its own.  Nothing is added by atomics: the order of every
+// sum follows the sorted places, so results repeat bit for bit.
 
 namespace engram {
 
-constexpr int kSortThreads = 256, kSortItems = 16, kSortTile = kSortThreads * kSortItems;
+constexpr int kSortThreads = 256, kSortItems = 8, kSortTile = kSortThreads * kSortItems;
+constexpr int kSortBits = 10;     // digit of the sort over many workgroups
+constexpr int kSmallThreads = 1024, kSmallItems = 16, kSmallSort = kSmallThreads * kSmallItems;
+constexpr int kSmallBits = 9;     // digit of the sort in one workgroup
 constexpr int kSegThreads = 256;
-constexpr int kJoin = 32;        // chunks per second-level chunk
-constexpr int kCountTile = 1024; // sorted places per workgroup of the run count
+constexpr int kUnit = 32;         // chunks per unit
+constexpr int kCountTile = 1024;  // sorted places per workgroup of the run count
 
 struct SortKArgs {
   const int32_t* ids;     // first pass: [T][ids_ld]
@@ -26,17 +34,16 @@ struct SortKArgs {
   const uint32_t* pos_in;
   uint32_t* key_out;
   uint32_t* pos_out;
-  uint32_t* hist;         // [256][blocks]
-  uint32_t* total;        // [256]
+  uint32_t* hist;         // [digits][blocks]
+  uint32_t* total;        // [digits]
   int64_t ids_ld;
-  uint32_t n, rows, cols, blocks, shift;
+  uint32_t n, rows, cols, blocks, shift, bits;
   FastDiv div_cols;
 };
 
 // the sort key of place i: its row, or `rows` where it has none
-template <bool FIRST, bool LATCH>
-__device__ __forceinline__ uint32_t sort_key(const SortKArgs& a, uint32_t i) {
-  if (!FIRST) return a.key_in[i];
+template <bool LATCH>
+__device__ __forceinline__ uint32_t place_key(const SortKArgs& a, uint32_t i) {
   const uint32_t t = fdiv(i, a.div_cols);
   const int32_t id = a.ids[(int64_t)t * a.ids_ld + (i - t * a.cols)];
   if (id >= 0 && (uint32_t)id < a.rows) return (uint32_t)id;
@@ -46,34 +53,41 @@ __device__ __forceinline__ uint32_t sort_key(const SortKArgs& a, uint32_t i) {
 
 template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortKArgs a) {
-  __shared__ uint32_t cnt[256];
-  cnt[threadIdx.x] = 0;
+  __shared__ uint32_t cnt[1 << kSortBits];
+  const uint32_t digits = 1u << a.bits;
+  for (uint32_t d = threadIdx.x; d < digits; d += kSortThreads) cnt[d] = 0;
   __syncthreads();
   const uint32_t base = blockIdx.x * kSortTile;
 #pragma unroll
   for (int i = 0; i < kSortItems; ++i) {
     const uint32_t at = base + i * kSortThreads + threadIdx.x;
-    if (at < a.n) atomicAdd(&cnt[(sort_key<FIRST, true>(a, at) >> a.shift) & 255u], 1u);
+    if (at < a.n) atomicAdd(&cnt[((FIRST ? place_key<true>(a, at) : a.key_in[at]) >> a.shift) & (digits - 1)], 1u);
   }
   __syncthreads();
-  a.hist[threadIdx.x * a.blocks + blockIdx.x] = cnt[threadIdx.x];
+  for (uint32_t d = threadIdx.x; d < digits; d += kSortThreads) a.hist[(int64_t)d * a.blocks + blockIdx.x] = cnt[d];
 }
 
-// exclusive sum over the 256 threads of a workgroup; *all receives the total
-__device__ __forceinline__ uint32_t scan256(uint32_t v, uint32_t* wsum, uint32_t* all) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t s = v;
+__device__ __forceinline__ uint32_t wave_inclusive(uint32_t v) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
-    const uint32_t o = (uint32_t)__shfl_up((int)s, off, 64);
-    if (lane >= off) s += o;
+    const uint32_t o = (uint32_t)__shfl_up((int)v, off, 64);
+    if (lane >= off) v += o;
   }
+  return v;
+}
+
+// exclusive sum over the workgroup's threads; *all receives the total
+template <int THREADS>
+__device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* wsum, uint32_t* all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t s = wave_inclusive(v);
   __syncthreads();  // the last call's readers are done with wsum
   if (lane == 63) wsum[wave] = s;
   __syncthreads();
   uint32_t before = 0, sum = 0;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < THREADS / 64; ++w) {
     if (w < wave) before += wsum[w];
     sum += wsum[w];
   }
@@ -81,75 +95,88 @@ __device__ __forceinline__ uint32_t scan256(uint32_t v, uint32_t* wsum, uint32_t
   return before + s - v;
 }
 
-// one workgroup per digit: its counts over the blocks become exclusive sums
+// one wave per digit: its counts over the blocks become exclusive sums
 __global__ __launch_bounds__(256) void sort_scan_kernel(SortKArgs a) {
-  __shared__ uint32_t wsum[4];
-  uint32_t* h = a.hist + (int64_t)blockIdx.x * a.blocks;
+  const uint32_t digit = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (digit >= 1u << a.bits) return;  // whole waves
+  uint32_t* h = a.hist + (int64_t)digit * a.blocks;
   uint32_t carry = 0;
-  for (uint32_t b = 0; b < a.blocks; b += 256) {
-    const uint32_t at = b + threadIdx.x;
+  for (uint32_t b = 0; b < a.blocks; b += 64) {
+    const uint32_t at = b + lane;
     const uint32_t v = at < a.blocks ? h[at] : 0u;
-    uint32_t all;
-    const uint32_t ex = scan256(v, wsum, &all);
-    if (at < a.blocks) h[at] = carry + ex;
-    carry += all;
+    const uint32_t s = wave_inclusive(v);
+    if (at < a.blocks) h[at] = carry + s - v;
+    carry += (uint32_t)__shfl((int)s, 63, 64);
   }
-  if (threadIdx.x == 0) a.total[blockIdx.x] = carry;
+  if (lane == 0) a.total[digit] = carry;
 }
 
-// Stable scatter of one pass: wave w owns places [1024 w, +1024) of the tile and ranks 64 of
-// them at a time; the lanes with one digit find each other by 8 ballots.
+// Stable rank of a wave's 64 keys among those with the same digit: the lanes with one digit
+// find each other by a ballot per bit, and the first of them moves the wave's count on.
+template <typename COUNT>
+__device__ __forceinline__ uint32_t wave_rank(uint32_t d, int bits, bool live, COUNT* cnt) {
+  uint64_t peers = __ballot(live);
+  for (int b = 0; b < bits; ++b) {  // uniform
+    const bool bit = (d >> b) & 1u;
+    const uint64_t m = __ballot(bit);
+    peers &= bit ? m : ~m;
+  }
+  const uint32_t below = (uint32_t)__popcll(peers & ((1ull << (threadIdx.x & 63)) - 1ull));
+  const uint32_t before = cnt[d];
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");  // every lane has read before one writes: LDS keeps a wave's order
+  if (live && below == 0) cnt[d] = (COUNT)(before + (uint32_t)__popcll(peers));
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+  return before + below;
+}
+
+// Stable scatter of one pass: wave w owns places [64 kSortItems w, + 64 kSortItems) of the tile
 template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortKArgs a) {
-  __shared__ uint32_t cnt[4][256];
+  constexpr int PER = (1 << kSortBits) / kSortThreads;  // digits per thread
+  __shared__ uint32_t cnt[4][1 << kSortBits];
   __shared__ uint32_t wsum[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) cnt[w][tid] = 0;
-  uint32_t all;
-  const uint32_t digit_base = scan256(a.total[tid], wsum, &all) + a.hist[(int64_t)tid * a.blocks + blockIdx.x];
-  __syncthreads();
+  const uint32_t digits = 1u << a.bits;
   uint32_t key[kSortItems], pos[kSortItems], rank[kSortItems];
   const uint32_t base = blockIdx.x * kSortTile + wave * (64 * kSortItems);
 #pragma unroll
   for (int i = 0; i < kSortItems; ++i) {
     const uint32_t at = base + i * 64 + lane;
-    key[i] = at < a.n ? sort_key<FIRST, false>(a, at) : 0u;
-    pos[i] = at < a.n ? (FIRST ? at : a.pos_in[at]) : 0u;
+    key[i] = at >= a.n ? 0u : FIRST ? place_key<false>(a, at) : a.key_in[at];
+    pos[i] = at >= a.n ? 0u : FIRST ? at : a.pos_in[at];
   }
+  uint32_t first[PER], sum = 0;  // thread's digits PER tid ..: first output place of this block
 #pragma unroll
-  for (int i = 0; i < kSortItems; ++i) {
-    const bool live = base + i * 64 + lane < a.n;
-    const uint32_t d = (key[i] >> a.shift) & 255u;
-    uint64_t peers = __ballot(live);
+  for (int e = 0; e < PER; ++e) {
+    const uint32_t d = tid * PER + e;
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      const bool bit = (d >> b) & 1u;
-      const uint64_t m = __ballot(bit);
-      peers &= bit ? m : ~m;
-    }
-    const uint32_t below = (uint32_t)__popcll(peers & ((1ull << lane) - 1ull));
-    const uint32_t before = cnt[wave][d];
-    __builtin_amdgcn_wave_barrier();
-    asm volatile("" ::: "memory");
-    if (live && below == 0) cnt[wave][d] = before + (uint32_t)__popcll(peers);
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_wave_barrier();
-    rank[i] = before + below;
+    for (int w = 0; w < 4; ++w) cnt[w][d] = 0;
+    first[e] = sum + (d < digits ? a.hist[(int64_t)d * a.blocks + blockIdx.x] : 0u);
+    sum += d < digits ? a.total[d] : 0u;
   }
+  uint32_t all;
+  const uint32_t before = block_exclusive<kSortThreads>(sum, wsum, &all);  // its barriers publish cnt
+#pragma unroll
+  for (int i = 0; i < kSortItems; ++i)
+    rank[i] = wave_rank((key[i] >> a.shift) & (digits - 1), (int)a.bits, base + i * 64 + lane < a.n, cnt[wave]);
   __syncthreads();
-  uint32_t run = digit_base;  // thread = digit: first output place of each wave's part
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const uint32_t c = cnt[w][tid];
-    cnt[w][tid] = run;
-    run += c;
+  for (int e = 0; e < PER; ++e) {
+    uint32_t run = before + first[e];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t c = cnt[w][tid * PER + e];
+      cnt[w][tid * PER + e] = run;
+      run += c;
+    }
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kSortItems; ++i) {
     if (base + i * 64 + lane >= a.n) continue;
-    const uint32_t to = cnt[wave][(key[i] >> a.shift) & 255u] + rank[i];
+    const uint32_t to = cnt[wave][(key[i] >> a.shift) & (digits - 1)] + rank[i];
     a.key_out[to] = key[i];
     a.pos_out[to] = pos[i];
   }
@@ -162,7 +189,7 @@ struct RunKArgs {
   uint32_t n, rows, ch, tiles;
   uint32_t* chunk_runs;  // runs that start in the chunk's tile before the chunk
   uint32_t* tile_runs;   // runs per tile, then exclusive sums
-  int32_t* unique;
+  int32_t* unique;       // null: no names wanted
   int32_t* count;
 };
 
@@ -179,7 +206,7 @@ __global__ __launch_bounds__(256) void run_count_kernel(RunKArgs a) {
     if (k < a.rows && (i == 0 || a.key[i - 1] != k)) ++c;
   }
   uint32_t all;
-  const uint32_t ex = scan256(c, wsum, &all);
+  const uint32_t ex = block_exclusive<256>(c, wsum, &all);
   if (i0 < a.n && i0 % a.ch == 0) a.chunk_runs[i0 / a.ch] = ex;
   if (threadIdx.x == 0) a.tile_runs[blockIdx.x] = all;
 }
@@ -191,11 +218,135 @@ __global__ __launch_bounds__(256) void run_scan_kernel(RunKArgs a) {
     const uint32_t at = b + threadIdx.x;
     const uint32_t v = at < a.tiles ? a.tile_runs[at] : 0u;
     uint32_t all;
-    const uint32_t ex = scan256(v, wsum, &all);
+    const uint32_t ex = block_exclusive<256>(v, wsum, &all);
     if (at < a.tiles) a.tile_runs[at] = carry + ex;
     carry += all;
   }
   if (threadIdx.x == 0) *a.count = (int32_t)carry;
+}
+
+// ---- the zeros of a dense gradient ----------------------------------------------------
+
+struct ZeroKArgs {
+  char* grad;
+  int64_t rows, row_bytes, ld_bytes;  // ld_bytes == row_bytes: one block of memory
+  int32_t vec;                        // rows start on 16 bytes
+};
+
+// workgroup `block` of `blocks`
+template <int THREADS>
+__device__ __forceinline__ void zero_rows(const ZeroKArgs& z, uint32_t block, uint32_t blocks) {
+  const u32x4 zero = {};
+  if (z.ld_bytes == z.row_bytes && ((uintptr_t)z.grad & 15) == 0) {
+    const int64_t bytes = z.rows * z.row_bytes, words = bytes / 16;
+    for (int64_t i = (int64_t)block * THREADS + threadIdx.x; i < words; i += (int64_t)blocks * THREADS)
+      __builtin_nontemporal_store(zero, reinterpret_cast<u32x4*>(z.grad) + i);
+    if (block == 0 && (int64_t)threadIdx.x < bytes - words * 16) z.grad[words * 16 + threadIdx.x] = 0;
+    return;
+  }
+  for (int64_t r = block; r < z.rows; r += blocks) {
+    char* row = z.grad + r * z.ld_bytes;
+    const int64_t words = z.vec ? z.row_bytes / 16 : 0;
+    for (int64_t i = threadIdx.x; i < words; i += THREADS) reinterpret_cast<u32x4*>(row)[i] = zero;
+    for (int64_t i = words * 16 + 2 * threadIdx.x; i < z.row_bytes; i += 2 * THREADS)
+      *reinterpret_cast<unsigned short*>(row + i) = 0;
+  }
+}
+
+__global__ __launch_bounds__(256) void zero_rows_kernel(ZeroKArgs z) { zero_rows<256>(z, blockIdx.x, gridDim.x); }
+
+// ---- a short list: sorted by one workgroup, in LDS -------------------------------------
+
+struct SmallSortLds {
+  uint32_t key[kSmallSort];
+  uint32_t pos[kSmallSort];
+  uint16_t cnt[kSmallThreads / 64][1 << kSmallBits];
+  uint32_t wsum[kSmallThreads / 64];
+};
+static_assert(sizeof(SmallSortLds) <= 160 * 1024, "one workgroup's LDS");
+
+__global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortKArgs a, RunKArgs r, ZeroKArgs z) {
+  if (blockIdx.x != 0) {
+    zero_rows<kSmallThreads>(z, blockIdx.x - 1, gridDim.x - 1);
+    return;
+  }
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  SmallSortLds& l = *reinterpret_cast<SmallSortLds*>(smem);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int WAVES = kSmallThreads / 64;
+  const int items = (int)((a.n + kSmallThreads - 1) / kSmallThreads);  // places per thread
+  const uint32_t base = (uint32_t)(wave * 64 * items + lane);
+  uint32_t key[kSmallItems], pos[kSmallItems], rank[kSmallItems];
+#pragma unroll
+  for (int i = 0; i < kSmallItems; ++i) {
+    const uint32_t at = base + i * 64;
+    const bool live = i < items && at < a.n;
+    key[i] = live ? place_key<true>(a, at) : 0u;
+    pos[i] = at;
+  }
+  const uint32_t digits = 1u << a.bits;
+  for (uint32_t shift = 0; shift == 0 || (a.rows >> shift) != 0; shift += a.bits) {  // uniform
+    if (shift != 0) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kSmallItems; ++i)
+        if (i < items && base + i * 64 < a.n) {
+          key[i] = l.key[base + i * 64];
+          pos[i] = l.pos[base + i * 64];
+        }
+    }
+    for (uint32_t d = tid; d < WAVES << a.bits; d += kSmallThreads) l.cnt[d >> a.bits][d & (digits - 1)] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSmallItems; ++i)
+      if (i < items)
+        rank[i] = wave_rank((key[i] >> shift) & (digits - 1), (int)a.bits, base + i * 64 < a.n, l.cnt[wave]);
+    __syncthreads();
+    uint32_t sum = 0;
+    if ((uint32_t)tid < digits) {
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        const uint32_t c = l.cnt[w][tid];
+        l.cnt[w][tid] = (uint16_t)sum;
+        sum += c;
+      }
+    }
+    uint32_t all;
+    const uint32_t before = block_exclusive<kSmallThreads>(sum, l.wsum, &all);
+    if ((uint32_t)tid < digits) {
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) l.cnt[w][tid] = (uint16_t)(l.cnt[w][tid] + before);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSmallItems; ++i)
+      if (i < items && base + i * 64 < a.n) {
+        const uint32_t to = l.cnt[wave][(key[i] >> shift) & (digits - 1)] + rank[i];
+        l.key[to] = key[i];
+        l.pos[to] = pos[i];
+      }
+  }
+  __syncthreads();
+  for (uint32_t i = tid; i < a.n; i += kSmallThreads) {
+    a.key_out[i] = l.key[i];
+    a.pos_out[i] = l.pos[i];
+    if (r.unique != nullptr) r.unique[i] = -1;
+  }
+  if (r.unique == nullptr) return;  // uniform
+  // runs: a thread's `span` consecutive places, whole chunks of 4
+  const uint32_t span = (uint32_t)((items + 3) / 4 * 4);
+  const uint32_t s0 = tid * span, s1 = min(a.n, s0 + span);
+  auto starts = [&](uint32_t i) { return l.key[i] < a.rows && (i == 0 || l.key[i - 1] != l.key[i]); };
+  uint32_t c = 0;
+  for (uint32_t i = s0; i < s1; ++i) c += starts(i) ? 1u : 0u;
+  uint32_t all;
+  uint32_t before = block_exclusive<kSmallThreads>(c, l.wsum, &all);
+  for (uint32_t i = s0; i < s1; ++i) {
+    if (i % r.ch == 0) r.chunk_runs[i / r.ch] = before;
+    before += starts(i) ? 1u : 0u;
+  }
+  if ((uint32_t)tid < r.tiles) r.tile_runs[tid] = 0;  // chunk_runs count from the start of the list
+  if (tid == 0) *r.count = (int32_t)all;
 }
 
 // ---- sums over the runs ------------------------------------------------------------
@@ -207,13 +358,12 @@ struct SegKArgs {
   void* grad;
   float* head;    // [chunks][pdim]
   float* tail;
-  float* head2;   // [chunks2][pdim]
-  float* tail2;
+  float* unit;    // [units][pdim]: sums of units inside one run
   const uint32_t* chunk_runs;
   const uint32_t* tile_runs;
   int32_t* unique;
   int64_t dout_ld, seg_pitch, grad_ld;
-  uint32_t n, rows, cols, ch, chunks, chunks2;
+  uint32_t n, rows, cols, ch, chunks, units;
   int32_t dim, pdim, mode;
   float scale;
   int32_t dout_vec, grad_vec;
@@ -222,7 +372,7 @@ struct SegKArgs {
 };
 
 struct SegPlace {
-  uint32_t unit;  // the chunk this group owns
+  uint32_t unit;  // the chunk (or unit) this group owns
   int32_t col;    // the lane's first column
 };
 
@@ -263,13 +413,27 @@ __device__ __forceinline__ void put_partial(float* to, const SegKArgs& a, uint32
   p[1] = f32x4{acc[4], acc[5], acc[6], acc[7]};
 }
 
-__device__ __forceinline__ void add_partial(const float* from, const SegKArgs& a, uint32_t unit, int32_t col, float* acc) {
-  const f32x4* p = reinterpret_cast<const f32x4*>(from + (int64_t)unit * a.pdim + col);
-  const f32x4 lo = p[0], hi = p[1];
+// acc += rows u0 .. u1 - 1 of a partial array, in order, eight in flight
+__device__ __forceinline__ void add_partials(const float* from, const SegKArgs& a, uint32_t u0, uint32_t u1, int32_t col,
+                                             float* acc) {
+  constexpr int U = 8;
+  for (uint32_t u = u0; u < u1; u += U) {
+    f32x4 v[U][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    acc[i] += lo[i];
-    acc[4 + i] += hi[i];
+    for (int e = 0; e < U; ++e) {
+      const f32x4* p = reinterpret_cast<const f32x4*>(from + (int64_t)min(u + e, u1 - 1) * a.pdim + col);
+      v[e][0] = p[0];
+      v[e][1] = p[1];
+    }
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      if (u + e >= u1) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i] += v[e][0][i];
+        acc[4 + i] += v[e][1][i];
+      }
+    }
   }
 }
 
@@ -278,156 +442,176 @@ __device__ __forceinline__ void clear8(float* acc) {
   for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
 }
 
+// 8 columns of a row as they are loaded, and as floats
+template <bool F32>
+struct RawChunk {
+  u32x4 w[F32 ? 2 : 1];
+  __device__ __forceinline__ void to_float(float* f) const {
+    if (F32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i >> 2][i & 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[0][i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[0][i] & 0xFFFF0000u);
+      }
+    }
+  }
+};
+
 template <bool DOUT_F32, bool GRAD_F32>
 __global__ __launch_bounds__(kSegThreads) void segment_sum_kernel(SegKArgs a) {
-  constexpr int U = 4;  // rows in flight per lane
+  constexpr int U = 8;  // rows in flight per lane
   const SegPlace p = seg_place(a);
   if (p.unit >= a.chunks || p.col >= a.dim) return;
   const uint32_t i0 = p.unit * a.ch, i1 = min(a.n, i0 + a.ch);
-  uint32_t cur = a.key[i0];
+  // (a.ch is a multiple of U) the next U places' keys and positions are fetched while the
+  // rows of the current ones are on their way
+  uint32_t nk[U], np[U];
+  auto fetch = [&](uint32_t i) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t at = min(i + u, a.n - 1);
+      nk[u] = a.key[at];
+      np[u] = a.pos[at];
+    }
+  };
+  const uint32_t left = a.key[max(i0, 1u) - 1], right = a.key[min(i1, a.n - 1)];
+  fetch(i0);
+  uint32_t cur = nk[0];
   if (cur >= a.rows) return;
-  bool started = i0 == 0 || a.key[i0 - 1] != cur;
+  bool started = i0 == 0 || left != cur;
   uint32_t run = 0;
   if (a.mode == ENGRAM_GRAD_SPARSE) run = runs_before(a, i0) - (started ? 0u : 1u);
   float acc[8];
   clear8(acc);
-  bool done = false;
-  for (uint32_t i = i0; i < i1 && !done; i += U) {
+  for (uint32_t i = i0; i < i1; i += U) {
     uint32_t k[U];
-    float f[U][8];
+    RawChunk<DOUT_F32> raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool live = i + u < i1;
-      k[u] = live ? a.key[i + u] : a.rows;
-      clear8(f[u]);
-      if (k[u] < a.rows) {
-        const uint32_t pos = a.pos[i + u];
-        const uint32_t t = fdiv(pos, a.div_cols);
+      k[u] = i + u < i1 ? nk[u] : a.rows;
+      const uint32_t t = fdiv(np[u], a.div_cols);
+      const int64_t at = (int64_t)t * a.dout_ld + (int64_t)(np[u] - t * a.cols) * a.seg_pitch + p.col;
+      if (a.dout_vec) {
         // columns up to the next multiple of 8 lie in the segment when it starts on 16 bytes
-        load_chunk8<DOUT_F32>(a.dout, (int64_t)t * a.dout_ld + (int64_t)(pos - t * a.cols) * a.seg_pitch + p.col,
-                              a.dout_vec ? 8 : min(8, a.dim - p.col), a.dout_vec != 0, f[u]);
+        const u32x4* src = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.dout) + at * (DOUT_F32 ? 4 : 2));
+        if (k[u] < a.rows) {
+          raw[u].w[0] = src[0];
+          if (DOUT_F32) raw[u].w[DOUT_F32 ? 1 : 0] = src[1];
+        }
+      } else if (k[u] < a.rows) {
+        float f[8];
+        load_chunk8<DOUT_F32>(a.dout, at, min(8, a.dim - p.col), false, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (DOUT_F32) raw[u].w[DOUT_F32 ? e >> 2 : 0][e & 3] = __float_as_uint(f[e]);
+          else if (e & 1) raw[u].w[0][e >> 1] |= __float_as_uint(f[e]);
+          else raw[u].w[0][e >> 1] = __float_as_uint(f[e]) >> 16;
+        }
       }
     }
+    if (i + U < i1) fetch(i + U);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i + u >= i1 || done) continue;
+      if (i + u >= i1) break;
       if (k[u] != cur) {
         if (started) write_row<GRAD_F32>(a, cur, run, p.col, acc);
         else put_partial(a.head, a, p.unit, p.col, acc);
+        if (k[u] >= a.rows) return;  // the rest has no row
         clear8(acc);
         started = true;
         cur = k[u];
         ++run;
-        if (cur >= a.rows) {
-          done = true;
-          continue;
-        }
       }
+      float f[8];
+      raw[u].to_float(f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += f[u][e];
+      for (int e = 0; e < 8; ++e) acc[e] += f[e];
     }
   }
-  if (done) return;
-  const bool goes_on = i1 < a.n && a.key[i1] == cur;
+  const bool goes_on = i1 < a.n && right == cur;
   if (!started) put_partial(a.head, a, p.unit, p.col, acc);
   else if (goes_on) put_partial(a.tail, a, p.unit, p.col, acc);
   else write_row<GRAD_F32>(a, cur, run, p.col, acc);
 }
 
-// whether the run of place i's left neighbour goes on at i (i > 0)
-__device__ __forceinline__ bool linked(const SegKArgs& a, uint32_t i) {
-  return i < a.n && a.key[i] < a.rows && a.key[i - 1] == a.key[i];
+// whether chunk c starts inside a run that came from the chunk before
+__device__ __forceinline__ bool comes_in(const SegKArgs& a, uint32_t c, uint32_t key) {
+  return c < a.chunks && a.key[c * a.ch] == key;
 }
 
-// the run index that a run reaching place i (the first of a chunk) from before has
-__device__ __forceinline__ uint32_t run_into(const SegKArgs& a, uint32_t i) {
-  return a.mode == ENGRAM_GRAD_SPARSE ? runs_before(a, i) - 1u : 0u;
-}
-
-// second level: one group per kJoin chunks
-template <bool GRAD_F32>
-__global__ __launch_bounds__(kSegThreads) void segment_join_kernel(SegKArgs a) {
+// sums of the units (kUnit chunks) that a run comes into and leaves: all of it is head rows
+__global__ __launch_bounds__(kSegThreads) void segment_unit_kernel(SegKArgs a) {
   const SegPlace p = seg_place(a);
-  if (p.unit >= a.chunks2 || p.col >= a.dim) return;
-  const uint32_t c0 = p.unit * kJoin, c1 = min(a.chunks, c0 + kJoin);
+  if (p.unit == 0 || p.unit >= a.units || p.col >= a.dim) return;
+  const uint32_t c0 = p.unit * kUnit, c1 = c0 + kUnit;
+  const uint32_t k = a.key[c0 * a.ch];
+  if (k >= a.rows || a.key[c0 * a.ch - 1] != k || !comes_in(a, c1, k)) return;
   float acc[8];
   clear8(acc);
-  bool in = c0 > 0 && linked(a, c0 * a.ch);
-  bool started = false;  // whether the open run started in this unit
-  for (uint32_t c = c0; c < c1; ++c) {
-    const uint32_t i0 = c * a.ch, i1 = min(a.n, i0 + a.ch);
-    const bool out = linked(a, i1);
-    const bool whole = a.key[i0] == a.key[i1 - 1];
-    if (in) {
-      add_partial(a.head, a, c, p.col, acc);
-      if (!(whole && out)) {  // the run ends in this chunk
-        if (started) write_row<GRAD_F32>(a, a.key[i0], run_into(a, i0), p.col, acc);
-        else put_partial(a.head2, a, p.unit, p.col, acc);
-      }
-    }
-    if (out && !(whole && in)) {  // a run starts here and goes on
-      clear8(acc);
-      add_partial(a.tail, a, c, p.col, acc);
-      started = true;
-    }
-    in = out;
-  }
-  if (!in) return;
-  if (started) put_partial(a.tail2, a, p.unit, p.col, acc);
-  else put_partial(a.head2, a, p.unit, p.col, acc);
+  add_partials(a.head, a, c0, c1, p.col, acc);
+  put_partial(a.unit, a, p.unit, p.col, acc);
 }
 
-// last level: the unit in which a run starts that leaves it adds what the following units hold
+// the chunk in which a run starts that leaves it adds what the following chunks hold
 template <bool GRAD_F32>
 __global__ __launch_bounds__(kSegThreads) void segment_finish_kernel(SegKArgs a) {
   const SegPlace p = seg_place(a);
-  if (p.unit >= a.chunks2 || p.col >= a.dim) return;
-  const uint32_t per = kJoin * a.ch;
-  const uint32_t i0 = p.unit * per;
-  if (a.n - i0 <= per) return;  // the last unit: nothing leaves it
-  const uint32_t end = i0 + per;
-  if (!linked(a, end)) return;
-  const uint32_t k = a.key[end];
-  if (p.unit > 0 && a.key[i0 - 1] == k) return;  // it started earlier
+  const uint32_t c = p.unit;
+  if (c + 1 >= a.chunks || p.col >= a.dim) return;
+  const uint32_t end = (c + 1) * a.ch;
+  const uint32_t k = a.key[end], inside = a.key[end - 1], before = a.key[max(c * a.ch, 1u) - 1];
+  if (k >= a.rows || inside != k) return;            // nothing leaves
+  if (c > 0 && before == k) return;                  // it started earlier
+  // the first chunk that the run does not come into: by doubling, then halving, steps
+  uint32_t lo = c + 1, step = 1;
+  while (comes_in(a, lo + step, k)) {
+    lo += step;
+    step *= 2;
+  }
+  for (; step > 1;) {
+    step /= 2;
+    if (comes_in(a, lo + step, k)) lo += step;
+  }
+  const uint32_t stop = lo + 1;
   float acc[8];
   clear8(acc);
-  add_partial(a.tail2, a, p.unit, p.col, acc);
-  uint32_t last = p.unit + 1;  // the unit in which the run ends
-  while (a.n - last * per > per && a.key[(last + 1) * per] == k) ++last;
-  for (uint32_t u = p.unit + 1; u <= last; ++u) add_partial(a.head2, a, u, p.col, acc);
-  write_row<GRAD_F32>(a, k, run_into(a, end), p.col, acc);
-}
-
-template <bool F32>
-__global__ __launch_bounds__(256) void zero_rows_kernel(void* grad, int64_t rows, int32_t dim, int64_t ld, int32_t vec,
-                                                        uint32_t chunks) {
-  const float z[8] = {};
-  const int64_t total = rows * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / chunks;
-    const int32_t col = (int32_t)(i - r * chunks) * 8;
-    store_chunk8<F32>(grad, r * ld + col, min(8, dim - col), vec != 0, z);
+  add_partials(a.tail, a, c, c + 1, p.col, acc);
+  // heads up to a unit, whole units (the run goes on behind them), heads of the rest
+  const uint32_t u0 = (c + kUnit) / kUnit, u1 = (stop - 1) / kUnit;
+  if (u0 < u1) {
+    add_partials(a.head, a, c + 1, u0 * kUnit, p.col, acc);
+    add_partials(a.unit, a, u0, u1, p.col, acc);
+    add_partials(a.head, a, u1 * kUnit, stop, p.col, acc);
+  } else {
+    add_partials(a.head, a, c + 1, stop, p.col, acc);
   }
+  const uint32_t run = a.mode == ENGRAM_GRAD_SPARSE ? runs_before(a, end) - 1u : 0u;
+  write_row<GRAD_F32>(a, k, run, p.col, acc);
 }
 
 // ---- the workspace and the launches -------------------------------------------------
 
 struct EmbedGradPlan {
-  uint32_t n, ch, chunks, chunks2, blocks, tiles;
+  uint32_t n, ch, chunks, units, blocks, tiles;
   int64_t pdim;
-  int64_t key[2], pos[2], hist, total, chunk_runs, tile_runs, head, tail, head2, tail2, bytes;
+  int64_t key[2], pos[2], hist, total, chunk_runs, tile_runs, head, tail, unit, bytes;
 };
 
 static EmbedGradPlan embed_grad_plan(int64_t n, int32_t dim) {
   EmbedGradPlan p;
   p.n = (uint32_t)n;
-  // places per chunk: few for short lists, so that they spread over the chip
-  p.ch = n <= 32768 ? 8 : 32;
+  p.pdim = ((int64_t)dim + 7) / 8 * 8;
+  // places per chunk: as many as leave enough lanes (each walks one chunk's 8 columns) for 8
+  // waves on every CU; more places make fewer partial rows
+  const int64_t lanes = n * (p.pdim / 8);
+  p.ch = lanes / 32 >= 131072 ? 32 : lanes / 16 >= 131072 ? 16 : 8;
   p.chunks = (uint32_t)((n + p.ch - 1) / p.ch);
-  p.chunks2 = (p.chunks + kJoin - 1) / kJoin;
+  p.units = (p.chunks + kUnit - 1) / kUnit;
   p.blocks = (uint32_t)((n + kSortTile - 1) / kSortTile);
   p.tiles = (uint32_t)((n + kCountTile - 1) / kCountTile);
-  p.pdim = (dim + 7) / 8 * 8;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;
@@ -438,14 +622,13 @@ static EmbedGradPlan embed_grad_plan(int64_t n, int32_t dim) {
     p.key[i] = take(4 * n);
     p.pos[i] = take(4 * n);
   }
-  p.hist = take(4ll * 256 * p.blocks);
-  p.total = take(4 * 256);
+  p.hist = take(4ll * (1 << kSortBits) * p.blocks);
+  p.total = take(4 << kSortBits);
   p.chunk_runs = take(4ll * p.chunks);
   p.tile_runs = take(4ll * p.tiles);
   p.head = take(4 * p.pdim * p.chunks);
   p.tail = take(4 * p.pdim * p.chunks);
-  p.head2 = take(4 * p.pdim * p.chunks2);
-  p.tail2 = take(4 * p.pdim * p.chunks2);
+  p.unit = take(4 * p.pdim * p.units);
   p.bytes = at;
   return p;
 }
@@ -459,40 +642,44 @@ template <bool GRAD_F32>
 static void launch_segments(const SegKArgs& a, int32_t dout_f32, hipStream_t stream) {
   const unsigned per = 256u >> a.group_shift;
   const unsigned cols = (unsigned)((a.dim + (8 << a.group_shift) - 1) / (8 << a.group_shift));
-  const dim3 block(kSegThreads), grid((a.chunks + per - 1) / per, cols), grid2((a.chunks2 + per - 1) / per, cols);
+  const dim3 block(kSegThreads), grid((a.chunks + per - 1) / per, cols);
   if (dout_f32)
     hipLaunchKernelGGL((segment_sum_kernel<true, GRAD_F32>), grid, block, 0, stream, a);
   else
     hipLaunchKernelGGL((segment_sum_kernel<false, GRAD_F32>), grid, block, 0, stream, a);
-  if (a.chunks > 1) hipLaunchKernelGGL((segment_join_kernel<GRAD_F32>), grid2, block, 0, stream, a);
-  if (a.chunks2 > 1) hipLaunchKernelGGL((segment_finish_kernel<GRAD_F32>), grid2, block, 0, stream, a);
+  if (a.units > 2)  // else no unit has one on either side
+    hipLaunchKernelGGL(segment_unit_kernel, dim3((a.units + per - 1) / per, cols), block, 0, stream, a);
+  if (a.chunks > 1) hipLaunchKernelGGL((segment_finish_kernel<GRAD_F32>), grid, block, 0, stream, a);
 }
 
 hipError_t launch_embed_grad(const EmbedGradArgs& g, hipStream_t stream) {
   (void)hipGetLastError();
   const size_t grad_size = g.grad_f32 ? 4 : 2, dout_size = g.dout_f32 ? 4 : 2;
   const int64_t n = g.T * g.cols;
+  const bool sparse = g.mode == ENGRAM_GRAD_SPARSE, dense = g.mode == ENGRAM_GRAD_DENSE;
   const int32_t grad_vec = ((uintptr_t)g.grad % 16 == 0 && g.grad_ld * grad_size % 16 == 0) ? 1 : 0;
-  if (g.mode == ENGRAM_GRAD_DENSE) {
-    const uint32_t chunks = (uint32_t)((g.dim + 7) / 8);
-    const int64_t blocks = (g.rows * chunks + 255) / 256;
-    const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
-    if (g.grad_f32)
-      hipLaunchKernelGGL((zero_rows_kernel<true>), grid, dim3(256), 0, stream, g.grad, g.rows, g.dim, g.grad_ld, grad_vec, chunks);
-    else
-      hipLaunchKernelGGL((zero_rows_kernel<false>), grid, dim3(256), 0, stream, g.grad, g.rows, g.dim, g.grad_ld, grad_vec, chunks);
+  ZeroKArgs z = {};
+  unsigned zero_blocks = 0;  // of 256 threads
+  if (dense) {
+    z.grad = static_cast<char*>(g.grad);
+    z.rows = g.rows;
+    z.row_bytes = (int64_t)g.dim * grad_size;
+    z.ld_bytes = g.grad_ld * grad_size;
+    z.vec = grad_vec;
+    const int64_t want = (g.rows * ((z.row_bytes + 15) / 16) + 1023) / 1024;  // 4 stores or more per thread
+    zero_blocks = (unsigned)(want < 1 ? 1 : want < 8192 ? want : 8192);
   }
   char* w = static_cast<char*>(g.work);
-  const EmbedGradPlan p = embed_grad_plan(n, g.dim);
-  RunKArgs r;
+  RunKArgs r = {};
   if (n == 0) {
-    if (g.mode == ENGRAM_GRAD_SPARSE) {
-      r = RunKArgs{};
+    if (dense) hipLaunchKernelGGL(zero_rows_kernel, dim3(zero_blocks), dim3(256), 0, stream, z);
+    if (sparse) {
       r.count = g.count;
       hipLaunchKernelGGL(run_scan_kernel, dim3(1), dim3(256), 0, stream, r);
     }
     return hipGetLastError();
   }
+  const EmbedGradPlan p = embed_grad_plan(n, g.dim);
 
   SortKArgs s;
   s.ids = g.ids;
@@ -504,45 +691,64 @@ hipError_t launch_embed_grad(const EmbedGradArgs& g, hipStream_t stream) {
   s.div_cols = make_fastdiv(s.cols);
   s.hist = reinterpret_cast<uint32_t*>(w + p.hist);
   s.total = reinterpret_cast<uint32_t*>(w + p.total);
+  r.n = p.n;
+  r.rows = s.rows;
+  r.ch = p.ch;
+  r.tiles = p.tiles;
+  r.chunk_runs = reinterpret_cast<uint32_t*>(w + p.chunk_runs);
+  r.tile_runs = reinterpret_cast<uint32_t*>(w + p.tile_runs);
+  r.unique = sparse ? g.unique : nullptr;
+  r.count = g.count;
+  // digits: the key's bits (keys go up to `rows`) in as few passes as the widest digit allows
+  uint32_t bits = 1;
+  while (bits < 32 && (s.rows >> bits) != 0) ++bits;
+  const bool small = n <= kSmallSort;
+  const uint32_t widest = small ? kSmallBits : kSortBits, passes = (bits + widest - 1) / widest;
+  s.bits = (bits + passes - 1) / passes;
   int cur = 0;
-  for (uint32_t shift = 0; shift < 32 && (shift == 0 || (s.rows >> shift) != 0); shift += 8) {
-    s.shift = shift;
-    s.key_in = reinterpret_cast<const uint32_t*>(w + p.key[cur]);
-    s.pos_in = reinterpret_cast<const uint32_t*>(w + p.pos[cur]);
-    cur ^= 1;
-    s.key_out = reinterpret_cast<uint32_t*>(w + p.key[cur]);
-    s.pos_out = reinterpret_cast<uint32_t*>(w + p.pos[cur]);
-    if (shift == 0) hipLaunchKernelGGL((sort_count_kernel<true>), dim3(p.blocks), dim3(kSortThreads), 0, stream, s);
-    else hipLaunchKernelGGL((sort_count_kernel<false>), dim3(p.blocks), dim3(kSortThreads), 0, stream, s);
-    hipLaunchKernelGGL(sort_scan_kernel, dim3(256), dim3(256), 0, stream, s);
-    if (shift == 0) hipLaunchKernelGGL((sort_scatter_kernel<true>), dim3(p.blocks), dim3(kSortThreads), 0, stream, s);
-    else hipLaunchKernelGGL((sort_scatter_kernel<false>), dim3(p.blocks), dim3(kSortThreads), 0, stream, s);
-  }
-  const uint32_t* key = reinterpret_cast<const uint32_t*>(w + p.key[cur]);
-  if (g.mode == ENGRAM_GRAD_SPARSE) {
-    r.key = key;
-    r.n = p.n;
-    r.rows = s.rows;
-    r.ch = p.ch;
-    r.tiles = p.tiles;
-    r.chunk_runs = reinterpret_cast<uint32_t*>(w + p.chunk_runs);
-    r.tile_runs = reinterpret_cast<uint32_t*>(w + p.tile_runs);
-    r.unique = g.unique;
-    r.count = g.count;
-    hipLaunchKernelGGL(run_count_kernel, dim3(p.tiles), dim3(256), 0, stream, r);
-    hipLaunchKernelGGL(run_scan_kernel, dim3(1), dim3(256), 0, stream, r);
+  if (small) {
+    s.shift = 0;
+    s.key_in = s.pos_in = nullptr;
+    s.key_out = reinterpret_cast<uint32_t*>(w + p.key[0]);
+    s.pos_out = reinterpret_cast<uint32_t*>(w + p.pos[0]);
+    static std::atomic<uint64_t> lds_set{0};
+    const hipError_t e =
+        ensure_dynamic_lds(reinterpret_cast<const void*>(&sort_small_kernel), (int)sizeof(SmallSortLds), lds_set);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(sort_small_kernel, dim3(1 + (zero_blocks + 3) / 4), dim3(kSmallThreads), sizeof(SmallSortLds), stream,
+                       s, r, z);
+  } else {
+    if (dense) hipLaunchKernelGGL(zero_rows_kernel, dim3(zero_blocks), dim3(256), 0, stream, z);
+    for (uint32_t pass = 0; pass < passes; ++pass) {
+      s.shift = pass * s.bits;
+      s.key_in = reinterpret_cast<const uint32_t*>(w + p.key[cur]);
+      s.pos_in = reinterpret_cast<const uint32_t*>(w + p.pos[cur]);
+      cur ^= 1;
+      s.key_out = reinterpret_cast<uint32_t*>(w + p.key[cur]);
+      s.pos_out = reinterpret_cast<uint32_t*>(w + p.pos[cur]);
+      const dim3 grid(p.blocks), block(kSortThreads);
+      if (pass == 0) hipLaunchKernelGGL((sort_count_kernel<true>), grid, block, 0, stream, s);
+      else hipLaunchKernelGGL((sort_count_kernel<false>), grid, block, 0, stream, s);
+      hipLaunchKernelGGL(sort_scan_kernel, dim3(((1u << s.bits) + 3) / 4), dim3(256), 0, stream, s);
+      if (pass == 0) hipLaunchKernelGGL((sort_scatter_kernel<true>), grid, block, 0, stream, s);
+      else hipLaunchKernelGGL((sort_scatter_kernel<false>), grid, block, 0, stream, s);
+    }
+    if (sparse) {
+      r.key = reinterpret_cast<const uint32_t*>(w + p.key[cur]);
+      hipLaunchKernelGGL(run_count_kernel, dim3(p.tiles), dim3(256), 0, stream, r);
+      hipLaunchKernelGGL(run_scan_kernel, dim3(1), dim3(256), 0, stream, r);
+    }
   }
   SegKArgs a;
-  a.key = key;
+  a.key = reinterpret_cast<const uint32_t*>(w + p.key[cur]);
   a.pos = reinterpret_cast<const uint32_t*>(w + p.pos[cur]);
   a.dout = g.dout;
   a.grad = g.grad;
   a.head = reinterpret_cast<float*>(w + p.head);
   a.tail = reinterpret_cast<float*>(w + p.tail);
-  a.head2 = reinterpret_cast<float*>(w + p.head2);
-  a.tail2 = reinterpret_cast<float*>(w + p.tail2);
-  a.chunk_runs = reinterpret_cast<const uint32_t*>(w + p.chunk_runs);
-  a.tile_runs = reinterpret_cast<const uint32_t*>(w + p.tile_runs);
+  a.unit = reinterpret_cast<float*>(w + p.unit);
+  a.chunk_runs = r.chunk_runs;
+  a.tile_runs = r.tile_runs;
   a.unique = g.unique;
   a.dout_ld = g.dout_ld;
   a.seg_pitch = g.seg_pitch;
@@ -552,7 +758,7 @@ hipError_t launch_embed_grad(const EmbedGradArgs& g, hipStream_t stream) {
   a.cols = s.cols;
   a.ch = p.ch;
   a.chunks = p.chunks;
-  a.chunks2 = p.chunks2;
+  a.units = p.units;
   a.dim = g.dim;
   a.pdim = (int32_t)p.pdim;
   a.mode = g.mode;
