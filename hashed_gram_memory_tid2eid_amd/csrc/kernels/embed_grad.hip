@@ -10,7 +10,8 @@
 // hides behind 2 GB of them); more take three launches for each digit of up to 10 bits.
 //
 // The sorted list is cut into chunks of `ch` places; a group of lanes owns one chunk and one
-// range of columns, 8 per lane, and walks it with fp32 sums in registers.  A run inside a
+// range of columns, 8 per lane (two runs of 4, so that fp32 rows are read and written in
+// whole lines), and walks it with fp32 sums in registers.  A run inside a
 // chunk is finished there and written once.  Runs that cross chunks leave partial rows:
 // `head` (a run that came in from the chunk before) and `tail` (a run that starts here and
 // goes on); the group of the chunk where such a run starts adds them up.  So that a row that
@@ -26,6 +27,7 @@ constexpr int kSmallThreads = 1024, kSmallItems = 16, kSmallSort = kSmallThreads
 constexpr int kSmallBits = 9;     // digit of the sort in one workgroup
 constexpr int kSegThreads = 256;
 constexpr int kUnit = 32;         // chunks per unit
+constexpr int kFewUnits = 16;     // up to this many units, runs add their heads without unit sums
 constexpr int kCountTile = 1024;  // sorted places per workgroup of the run count
 
 struct SortKArgs {
@@ -112,9 +114,10 @@ __global__ __launch_bounds__(256) void sort_scan_kernel(SortKArgs a) {
 }
 
 // Stable rank of a wave's 64 keys among those with the same digit: the lanes with one digit
-// find each other by a ballot per bit, and the first of them moves the wave's count on.
+// find each other by a ballot per bit, and the first of them moves the wave's count of the
+// digit on.
 template <typename COUNT>
-__device__ __forceinline__ uint32_t wave_rank(uint32_t d, int bits, bool live, COUNT* cnt) {
+__device__ __forceinline__ uint32_t wave_rank(uint32_t d, int bits, bool live, COUNT* count) {
   uint64_t peers = __ballot(live);
   for (int b = 0; b < bits; ++b) {  // uniform
     const bool bit = (d >> b) & 1u;
@@ -122,10 +125,10 @@ __device__ __forceinline__ uint32_t wave_rank(uint32_t d, int bits, bool live, C
     peers &= bit ? m : ~m;
   }
   const uint32_t below = (uint32_t)__popcll(peers & ((1ull << (threadIdx.x & 63)) - 1ull));
-  const uint32_t before = cnt[d];
+  const uint32_t before = *count;
   __builtin_amdgcn_wave_barrier();
   asm volatile("" ::: "memory");  // every lane has read before one writes: LDS keeps a wave's order
-  if (live && below == 0) cnt[d] = (COUNT)(before + (uint32_t)__popcll(peers));
+  if (live && below == 0) *count = (COUNT)(before + (uint32_t)__popcll(peers));
   asm volatile("" ::: "memory");
   __builtin_amdgcn_wave_barrier();
   return before + below;
@@ -159,8 +162,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortKArgs a)
   uint32_t all;
   const uint32_t before = block_exclusive<kSortThreads>(sum, wsum, &all);  // its barriers publish cnt
 #pragma unroll
-  for (int i = 0; i < kSortItems; ++i)
-    rank[i] = wave_rank((key[i] >> a.shift) & (digits - 1), (int)a.bits, base + i * 64 + lane < a.n, cnt[wave]);
+  for (int i = 0; i < kSortItems; ++i) {
+    const uint32_t d = (key[i] >> a.shift) & (digits - 1);
+    rank[i] = wave_rank(d, (int)a.bits, base + i * 64 + lane < a.n, &cnt[wave][d]);
+  }
   __syncthreads();
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
@@ -240,7 +245,7 @@ __device__ __forceinline__ void zero_rows(const ZeroKArgs& z, uint32_t block, ui
   if (z.ld_bytes == z.row_bytes && ((uintptr_t)z.grad & 15) == 0) {
     const int64_t bytes = z.rows * z.row_bytes, words = bytes / 16;
     for (int64_t i = (int64_t)block * THREADS + threadIdx.x; i < words; i += (int64_t)blocks * THREADS)
-      __builtin_nontemporal_store(zero, reinterpret_cast<u32x4*>(z.grad) + i);
+      reinterpret_cast<u32x4*>(z.grad)[i] = zero;
     if (block == 0 && (int64_t)threadIdx.x < bytes - words * 16) z.grad[words * 16 + threadIdx.x] = 0;
     return;
   }
@@ -260,7 +265,7 @@ __global__ __launch_bounds__(256) void zero_rows_kernel(ZeroKArgs z) { zero_rows
 struct SmallSortLds {
   uint32_t key[kSmallSort];
   uint32_t pos[kSmallSort];
-  uint16_t cnt[kSmallThreads / 64][1 << kSmallBits];
+  uint16_t cnt[(kSmallThreads / 64) << kSmallBits];  // [digit][wave]
   uint32_t wsum[kSmallThreads / 64];
 };
 static_assert(sizeof(SmallSortLds) <= 160 * 1024, "one workgroup's LDS");
@@ -295,33 +300,36 @@ __global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortKArgs a, 
           pos[i] = l.pos[base + i * 64];
         }
     }
-    for (uint32_t d = tid; d < WAVES << a.bits; d += kSmallThreads) l.cnt[d >> a.bits][d & (digits - 1)] = 0;
+    // a thread's counters: `per` of the (digit, wave) list, whose exclusive sums are the first
+    // output places
+    const uint32_t per = max(1u, (uint32_t)(WAVES << a.bits) / kSmallThreads), c0 = tid * per;
+    const bool counts = c0 < (uint32_t)(WAVES << a.bits);
+    if (counts)
+      for (uint32_t e = 0; e < per; ++e) l.cnt[c0 + e] = 0;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kSmallItems; ++i)
-      if (i < items)
-        rank[i] = wave_rank((key[i] >> shift) & (digits - 1), (int)a.bits, base + i * 64 < a.n, l.cnt[wave]);
+      if (i < items) {
+        const uint32_t d = (key[i] >> shift) & (digits - 1);
+        rank[i] = wave_rank(d, (int)a.bits, base + i * 64 < a.n, &l.cnt[d * WAVES + wave]);
+      }
     __syncthreads();
     uint32_t sum = 0;
-    if ((uint32_t)tid < digits) {
-#pragma unroll
-      for (int w = 0; w < WAVES; ++w) {
-        const uint32_t c = l.cnt[w][tid];
-        l.cnt[w][tid] = (uint16_t)sum;
-        sum += c;
-      }
-    }
+    if (counts)
+      for (uint32_t e = 0; e < per; ++e) sum += l.cnt[c0 + e];
     uint32_t all;
-    const uint32_t before = block_exclusive<kSmallThreads>(sum, l.wsum, &all);
-    if ((uint32_t)tid < digits) {
-#pragma unroll
-      for (int w = 0; w < WAVES; ++w) l.cnt[w][tid] = (uint16_t)(l.cnt[w][tid] + before);
-    }
+    uint32_t before = block_exclusive<kSmallThreads>(sum, l.wsum, &all);
+    if (counts)
+      for (uint32_t e = 0; e < per; ++e) {
+        const uint32_t c = l.cnt[c0 + e];
+        l.cnt[c0 + e] = (uint16_t)before;
+        before += c;
+      }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kSmallItems; ++i)
       if (i < items && base + i * 64 < a.n) {
-        const uint32_t to = l.cnt[wave][(key[i] >> shift) & (digits - 1)] + rank[i];
+        const uint32_t to = l.cnt[((key[i] >> shift) & (digits - 1)) * WAVES + wave] + rank[i];
         l.key[to] = key[i];
         l.pos[to] = pos[i];
       }
@@ -373,14 +381,16 @@ struct SegKArgs {
 
 struct SegPlace {
   uint32_t unit;  // the chunk (or unit) this group owns
-  int32_t col;    // the lane's first column
+  int32_t col;    // the lane's first 4 columns; its other 4 are `other` columns on
+  int32_t other;
 };
 
 __device__ __forceinline__ SegPlace seg_place(const SegKArgs& a) {
   const uint32_t lane = threadIdx.x & ((1u << a.group_shift) - 1u);
   SegPlace p;
   p.unit = (blockIdx.x << (8 - a.group_shift)) + (threadIdx.x >> a.group_shift);
-  p.col = (int32_t)(((blockIdx.y << a.group_shift) + lane) * 8);
+  p.other = 4 << a.group_shift;
+  p.col = (int32_t)(blockIdx.y * 2 * p.other + lane * 4);
   return p;
 }
 
@@ -390,50 +400,58 @@ __device__ __forceinline__ uint32_t runs_before(const SegKArgs& a, uint32_t i) {
 }
 
 template <bool GRAD_F32>
-__device__ __forceinline__ void write_row(const SegKArgs& a, uint32_t key, uint32_t run, int32_t col, const float* acc) {
-  const int n = min(8, a.dim - col);
-  float f[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = acc[i] * a.scale;
+__device__ __forceinline__ void write_row(const SegKArgs& a, uint32_t key, uint32_t run, const SegPlace& p, const float* acc) {
   const bool sparse = a.mode == ENGRAM_GRAD_SPARSE;
-  const int64_t at = (int64_t)(sparse ? run : key) * a.grad_ld + col;
-  if (sparse && col == 0) a.unique[run] = (int32_t)key;
-  if (a.mode == ENGRAM_GRAD_ACCUMULATE) {
-    float old[8];
-    load_chunk8<GRAD_F32>(a.grad, at, n, a.grad_vec != 0, old);
+  const int64_t row = (int64_t)(sparse ? run : key) * a.grad_ld;
+  if (sparse && p.col == 0) a.unique[run] = (int32_t)key;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] += old[i];
+  for (int h = 0; h < 2; ++h) {
+    const int32_t col = p.col + h * p.other;
+    const int n = min(4, a.dim - col);
+    if (n <= 0) continue;
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = acc[4 * h + i] * a.scale;
+    if (a.mode == ENGRAM_GRAD_ACCUMULATE) {
+      float old[4];
+      load_chunk<GRAD_F32, 4>(a.grad, row + col, n, a.grad_vec != 0, old);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] += old[i];
+    }
+    // past the caches, which keep dout's rows: 16,384 x 24 places of 256 171 us against 198
+    store_chunk<GRAD_F32, 4, true>(a.grad, row + col, n, a.grad_vec != 0, f);
   }
-  store_chunk8<GRAD_F32>(a.grad, at, n, a.grad_vec != 0, f);
 }
 
-__device__ __forceinline__ void put_partial(float* to, const SegKArgs& a, uint32_t unit, int32_t col, const float* acc) {
-  f32x4* p = reinterpret_cast<f32x4*>(to + (int64_t)unit * a.pdim + col);
-  p[0] = f32x4{acc[0], acc[1], acc[2], acc[3]};
-  p[1] = f32x4{acc[4], acc[5], acc[6], acc[7]};
+// partial rows are padded to whole lanes' columns
+__device__ __forceinline__ void put_partial(float* to, const SegKArgs& a, const SegPlace& p, const float* acc) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    *reinterpret_cast<f32x4*>(to + (int64_t)p.unit * a.pdim + p.col + h * p.other) =
+        f32x4{acc[4 * h], acc[4 * h + 1], acc[4 * h + 2], acc[4 * h + 3]};
 }
 
-// acc += rows u0 .. u1 - 1 of a partial array, in order, eight in flight
-__device__ __forceinline__ void add_partials(const float* from, const SegKArgs& a, uint32_t u0, uint32_t u1, int32_t col,
-                                             float* acc) {
-  constexpr int U = 8;
+// acc += rows u0 .. u1 - 1 of a partial array, in order, many in flight
+__device__ __forceinline__ void add_partials(const float* from, const SegKArgs& a, uint32_t u0, uint32_t u1,
+                                             const SegPlace& p, float* acc) {
+  constexpr int U = 16;
   for (uint32_t u = u0; u < u1; u += U) {
     f32x4 v[U][2];
 #pragma unroll
     for (int e = 0; e < U; ++e) {
-      const f32x4* p = reinterpret_cast<const f32x4*>(from + (int64_t)min(u + e, u1 - 1) * a.pdim + col);
-      v[e][0] = p[0];
-      v[e][1] = p[1];
+      const float* src = from + (int64_t)min(u + e, u1 - 1) * a.pdim + p.col;
+      v[e][0] = *reinterpret_cast<const f32x4*>(src);
+      v[e][1] = *reinterpret_cast<const f32x4*>(src + p.other);
     }
 #pragma unroll
-    for (int e = 0; e < U; ++e) {
-      if (u + e >= u1) break;
+    for (int e = 0; e < U; ++e)
+      if (u + e < u1) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i] += v[e][0][i];
-        acc[4 + i] += v[e][1][i];
+        for (int i = 0; i < 4; ++i) {
+          acc[i] += v[e][0][i];
+          acc[4 + i] += v[e][1][i];
+        }
       }
-    }
   }
 }
 
@@ -442,19 +460,51 @@ __device__ __forceinline__ void clear8(float* acc) {
   for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
 }
 
-// 8 columns of a row as they are loaded, and as floats
+// a lane's 8 columns of a row as they are loaded, and as floats
 template <bool F32>
 struct RawChunk {
-  u32x4 w[F32 ? 2 : 1];
+  uint32_t w[F32 ? 8 : 4];
+  // vec: segments start on 16 bytes and hold the columns up to the next multiple of 4
+  __device__ __forceinline__ void load(const void* base, int64_t row, const SegPlace& p, int32_t dim, bool vec) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int32_t col = p.col + h * p.other;
+      const int64_t at = row + col;
+      if (col >= dim) {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 4 : 2); ++i) w[(F32 ? 4 : 2) * h + i] = 0u;
+      } else if (vec) {
+        if (F32) {
+          const u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + at);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[F32 ? 4 * h + i : 0] = v[i];
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(base) + at);
+          w[2 * h] = v.x;
+          w[2 * h + 1] = v.y;
+        }
+      } else {
+        float f[4];
+        load_chunk<F32, 4>(base, at, dim - col, false, f);
+        if (F32) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[F32 ? 4 * h + i : 0] = __float_as_uint(f[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) w[2 * h + i] = (__float_as_uint(f[2 * i]) >> 16) | __float_as_uint(f[2 * i + 1]);
+        }
+      }
+    }
+  }
   __device__ __forceinline__ void to_float(float* f) const {
     if (F32) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i >> 2][i & 3]);
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[F32 ? i : 0]);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[0][i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[0][i] & 0xFFFF0000u);
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
       }
     }
   }
@@ -493,32 +543,16 @@ __global__ __launch_bounds__(kSegThreads) void segment_sum_kernel(SegKArgs a) {
     for (int u = 0; u < U; ++u) {
       k[u] = i + u < i1 ? nk[u] : a.rows;
       const uint32_t t = fdiv(np[u], a.div_cols);
-      const int64_t at = (int64_t)t * a.dout_ld + (int64_t)(np[u] - t * a.cols) * a.seg_pitch + p.col;
-      if (a.dout_vec) {
-        // columns up to the next multiple of 8 lie in the segment when it starts on 16 bytes
-        const u32x4* src = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.dout) + at * (DOUT_F32 ? 4 : 2));
-        if (k[u] < a.rows) {
-          raw[u].w[0] = src[0];
-          if (DOUT_F32) raw[u].w[DOUT_F32 ? 1 : 0] = src[1];
-        }
-      } else if (k[u] < a.rows) {
-        float f[8];
-        load_chunk8<DOUT_F32>(a.dout, at, min(8, a.dim - p.col), false, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (DOUT_F32) raw[u].w[DOUT_F32 ? e >> 2 : 0][e & 3] = __float_as_uint(f[e]);
-          else if (e & 1) raw[u].w[0][e >> 1] |= __float_as_uint(f[e]);
-          else raw[u].w[0][e >> 1] = __float_as_uint(f[e]) >> 16;
-        }
-      }
+      const int64_t row = (int64_t)t * a.dout_ld + (int64_t)(np[u] - t * a.cols) * a.seg_pitch;
+      if (k[u] < a.rows) raw[u].load(a.dout, row, p, a.dim, a.dout_vec != 0);
     }
     if (i + U < i1) fetch(i + U);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i + u >= i1) break;
+      if (i + u >= i1) continue;
       if (k[u] != cur) {
-        if (started) write_row<GRAD_F32>(a, cur, run, p.col, acc);
-        else put_partial(a.head, a, p.unit, p.col, acc);
+        if (started) write_row<GRAD_F32>(a, cur, run, p, acc);
+        else put_partial(a.head, a, p, acc);
         if (k[u] >= a.rows) return;  // the rest has no row
         clear8(acc);
         started = true;
@@ -532,9 +566,9 @@ __global__ __launch_bounds__(kSegThreads) void segment_sum_kernel(SegKArgs a) {
     }
   }
   const bool goes_on = i1 < a.n && right == cur;
-  if (!started) put_partial(a.head, a, p.unit, p.col, acc);
-  else if (goes_on) put_partial(a.tail, a, p.unit, p.col, acc);
-  else write_row<GRAD_F32>(a, cur, run, p.col, acc);
+  if (!started) put_partial(a.head, a, p, acc);
+  else if (goes_on) put_partial(a.tail, a, p, acc);
+  else write_row<GRAD_F32>(a, cur, run, p, acc);
 }
 
 // whether chunk c starts inside a run that came from the chunk before
@@ -551,8 +585,8 @@ __global__ __launch_bounds__(kSegThreads) void segment_unit_kernel(SegKArgs a) {
   if (k >= a.rows || a.key[c0 * a.ch - 1] != k || !comes_in(a, c1, k)) return;
   float acc[8];
   clear8(acc);
-  add_partials(a.head, a, c0, c1, p.col, acc);
-  put_partial(a.unit, a, p.unit, p.col, acc);
+  add_partials(a.head, a, c0, c1, p, acc);
+  put_partial(a.unit, a, p, acc);
 }
 
 // the chunk in which a run starts that leaves it adds what the following chunks hold
@@ -560,42 +594,44 @@ template <bool GRAD_F32>
 __global__ __launch_bounds__(kSegThreads) void segment_finish_kernel(SegKArgs a) {
   const SegPlace p = seg_place(a);
   const uint32_t c = p.unit;
-  if (c + 1 >= a.chunks || p.col >= a.dim) return;
+  if (c + 1 >= a.chunks) return;  // lanes past the row's columns stay: they look for the end, too
   const uint32_t end = (c + 1) * a.ch;
   const uint32_t k = a.key[end], inside = a.key[end - 1], before = a.key[max(c * a.ch, 1u) - 1];
-  if (k >= a.rows || inside != k) return;            // nothing leaves
-  if (c > 0 && before == k) return;                  // it started earlier
-  // the first chunk that the run does not come into: by doubling, then halving, steps
-  uint32_t lo = c + 1, step = 1;
-  while (comes_in(a, lo + step, k)) {
-    lo += step;
-    step *= 2;
+  if (k >= a.rows || inside != k) return;  // nothing leaves (the same for the whole group)
+  if (c > 0 && before == k) return;        // it started earlier
+  // `stop`, the first chunk that the run does not come into: the lanes of the group (of the
+  // wave, where the group is larger) look at as many chunks at once
+  const uint32_t width = min(64u, 1u << a.group_shift), me = threadIdx.x & (width - 1);
+  const uint64_t mine = (width == 64 ? ~0ull : ((1ull << width) - 1ull)) << (threadIdx.x & 63 & ~(width - 1));
+  uint32_t stop = c + 2;
+  for (;;) {
+    const uint64_t ended = __ballot(!comes_in(a, stop + me, k)) & mine;
+    if (ended != 0) {
+      stop += (uint32_t)(__ffsll((unsigned long long)(ended >> (threadIdx.x & 63 & ~(width - 1)))) - 1);
+      break;
+    }
+    stop += width;
   }
-  for (; step > 1;) {
-    step /= 2;
-    if (comes_in(a, lo + step, k)) lo += step;
-  }
-  const uint32_t stop = lo + 1;
   float acc[8];
   clear8(acc);
-  add_partials(a.tail, a, c, c + 1, p.col, acc);
+  add_partials(a.tail, a, c, c + 1, p, acc);
   // heads up to a unit, whole units (the run goes on behind them), heads of the rest
   const uint32_t u0 = (c + kUnit) / kUnit, u1 = (stop - 1) / kUnit;
-  if (u0 < u1) {
-    add_partials(a.head, a, c + 1, u0 * kUnit, p.col, acc);
-    add_partials(a.unit, a, u0, u1, p.col, acc);
-    add_partials(a.head, a, u1 * kUnit, stop, p.col, acc);
+  if (a.units > kFewUnits && u0 < u1) {
+    add_partials(a.head, a, c + 1, u0 * kUnit, p, acc);
+    add_partials(a.unit, a, u0, u1, p, acc);
+    add_partials(a.head, a, u1 * kUnit, stop, p, acc);
   } else {
-    add_partials(a.head, a, c + 1, stop, p.col, acc);
+    add_partials(a.head, a, c + 1, stop, p, acc);
   }
   const uint32_t run = a.mode == ENGRAM_GRAD_SPARSE ? runs_before(a, end) - 1u : 0u;
-  write_row<GRAD_F32>(a, k, run, p.col, acc);
+  write_row<GRAD_F32>(a, k, run, p, acc);
 }
 
 // ---- the workspace and the launches -------------------------------------------------
 
 struct EmbedGradPlan {
-  uint32_t n, ch, chunks, units, blocks, tiles;
+  uint32_t n, ch, chunks, units, blocks, tiles, shift;
   int64_t pdim;
   int64_t key[2], pos[2], hist, total, chunk_runs, tile_runs, head, tail, unit, bytes;
 };
@@ -603,7 +639,11 @@ struct EmbedGradPlan {
 static EmbedGradPlan embed_grad_plan(int64_t n, int32_t dim) {
   EmbedGradPlan p;
   p.n = (uint32_t)n;
-  p.pdim = ((int64_t)dim + 7) / 8 * 8;
+  // partial rows hold whole groups' columns
+  p.shift = 2;
+  while (p.shift < 8 && (8 << p.shift) < dim) ++p.shift;
+  const int64_t group = 8 << p.shift;
+  p.pdim = ((int64_t)dim + group - 1) / group * group;
   // places per chunk: as many as leave enough lanes (each walks one chunk's 8 columns) for 8
   // waves on every CU; more places make fewer partial rows
   const int64_t lanes = n * (p.pdim / 8);
@@ -647,7 +687,7 @@ static void launch_segments(const SegKArgs& a, int32_t dout_f32, hipStream_t str
     hipLaunchKernelGGL((segment_sum_kernel<true, GRAD_F32>), grid, block, 0, stream, a);
   else
     hipLaunchKernelGGL((segment_sum_kernel<false, GRAD_F32>), grid, block, 0, stream, a);
-  if (a.units > 2)  // else no unit has one on either side
+  if (a.units > kFewUnits)
     hipLaunchKernelGGL(segment_unit_kernel, dim3((a.units + per - 1) / per, cols), block, 0, stream, a);
   if (a.chunks > 1) hipLaunchKernelGGL((segment_finish_kernel<GRAD_F32>), grid, block, 0, stream, a);
 }
@@ -764,13 +804,12 @@ hipError_t launch_embed_grad(const EmbedGradArgs& g, hipStream_t stream) {
   a.mode = g.mode;
   a.scale = g.scale;
   a.dout_vec = ((uintptr_t)g.dout % 16 == 0 && g.dout_ld * dout_size % 16 == 0 && g.seg_pitch * dout_size % 16 == 0 &&
-                g.seg_pitch >= p.pdim)
+                g.seg_pitch >= ((int64_t)g.dim + 3) / 4 * 4)
                    ? 1
                    : 0;
   a.grad_vec = grad_vec;
   a.div_cols = s.div_cols;
-  a.group_shift = 2;
-  while (a.group_shift < 8 && (8 << a.group_shift) < g.dim) ++a.group_shift;
+  a.group_shift = p.shift;
   if (g.grad_f32) launch_segments<true>(a, g.dout_f32, stream);
   else launch_segments<false>(a, g.dout_f32, stream);
   return hipGetLastError();

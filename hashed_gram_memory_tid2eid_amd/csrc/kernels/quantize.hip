@@ -99,7 +99,7 @@ __global__ __launch_bounds__(kQuantThreads) void fp8_quantize_kernel(QuantKArgs 
   for (int i = 0; i < RT; ++i) {
     const int64_t m = m0 + r0 + i;
     if (m < a.M && nk > 0) {
-      load_chunk8<X_F32>(a.x, m * a.ld + k0, nk, a.vec != 0, x[i]);
+      load_chunk<X_F32, 8>(a.x, m * a.ld + k0, nk, a.vec != 0, x[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[i][j] = 0.0f;
