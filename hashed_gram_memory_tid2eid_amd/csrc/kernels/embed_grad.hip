@@ -434,7 +434,7 @@ __device__ __forceinline__ void put_partial(float* to, const SegKArgs& a, const 
 // acc += rows u0 .. u1 - 1 of a partial array, in order, many in flight
 __device__ __forceinline__ void add_partials(const float* from, const SegKArgs& a, uint32_t u0, uint32_t u1,
                                              const SegPlace& p, float* acc) {
-  constexpr int U = 16;
+  constexpr int U = 8;
   for (uint32_t u = u0; u < u1; u += U) {
     f32x4 v[U][2];
 #pragma unroll
@@ -512,7 +512,7 @@ struct RawChunk {
 
 template <bool DOUT_F32, bool GRAD_F32>
 __global__ __launch_bounds__(kSegThreads) void segment_sum_kernel(SegKArgs a) {
-  constexpr int U = 8;  // rows in flight per lane
+  constexpr int U = 4;  // rows in flight per lane
   const SegPlace p = seg_place(a);
   if (p.unit >= a.chunks || p.col >= a.dim) return;
   const uint32_t i0 = p.unit * a.ch, i1 = min(a.n, i0 + a.ch);
@@ -571,18 +571,14 @@ __global__ __launch_bounds__(kSegThreads) void segment_sum_kernel(SegKArgs a) {
   else write_row<GRAD_F32>(a, cur, run, p, acc);
 }
 
-// whether chunk c starts inside a run that came from the chunk before
-__device__ __forceinline__ bool comes_in(const SegKArgs& a, uint32_t c, uint32_t key) {
-  return c < a.chunks && a.key[c * a.ch] == key;
-}
-
 // sums of the units (kUnit chunks) that a run comes into and leaves: all of it is head rows
 __global__ __launch_bounds__(kSegThreads) void segment_unit_kernel(SegKArgs a) {
   const SegPlace p = seg_place(a);
   if (p.unit == 0 || p.unit >= a.units || p.col >= a.dim) return;
   const uint32_t c0 = p.unit * kUnit, c1 = c0 + kUnit;
   const uint32_t k = a.key[c0 * a.ch];
-  if (k >= a.rows || a.key[c0 * a.ch - 1] != k || !comes_in(a, c1, k)) return;
+  if (k >= a.rows || a.key[c0 * a.ch - 1] != k || c1 >= a.chunks || a.key[c1 * a.ch] != k)
+    return;
   float acc[8];
   clear8(acc);
   add_partials(a.head, a, c0, c1, p, acc);
@@ -600,17 +596,20 @@ __global__ __launch_bounds__(kSegThreads) void segment_finish_kernel(SegKArgs a)
   if (k >= a.rows || inside != k) return;  // nothing leaves (the same for the whole group)
   if (c > 0 && before == k) return;        // it started earlier
   // `stop`, the first chunk that the run does not come into: the lanes of the group (of the
-  // wave, where the group is larger) look at as many chunks at once
-  const uint32_t width = min(64u, 1u << a.group_shift), me = threadIdx.x & (width - 1);
-  const uint64_t mine = (width == 64 ? ~0ull : ((1ull << width) - 1ull)) << (threadIdx.x & 63 & ~(width - 1));
-  uint32_t stop = c + 2;
+  // wave, where the group is larger) each look at the last chunk of a block of `step`; while
+  // the run covers all blocks they grow, then the block that it ends in is divided
+  const uint32_t shift = min(6u, a.group_shift), width = 1u << shift, lane = threadIdx.x & 63;
+  const uint32_t me = lane & (width - 1), lowest = lane & ~(width - 1);
+  uint32_t stop = c + 2, step = 0;  // step: log2
   for (;;) {
-    const uint64_t ended = __ballot(!comes_in(a, stop + me, k)) & mine;
-    if (ended != 0) {
-      stop += (uint32_t)(__ffsll((unsigned long long)(ended >> (threadIdx.x & 63 & ~(width - 1)))) - 1);
-      break;
-    }
-    stop += width;
+    const uint64_t at = (uint64_t)stop + ((uint64_t)(me + 1) << step) - 1;
+    const bool covered = at < a.chunks && a.key[(uint32_t)at * a.ch] == k;
+    const uint64_t ended = (__ballot(!covered) >> lowest) & (width == 64 ? ~0ull : (1ull << width) - 1ull);
+    const uint32_t blocks = ended != 0 ? (uint32_t)__ffsll((unsigned long long)ended) - 1 : width;
+    stop += blocks << step;
+    if (ended == 0) step += shift;
+    else if (step == 0) break;
+    else step -= shift;
   }
   float acc[8];
   clear8(acc);
