@@ -314,12 +314,141 @@ __global__ __launch_bounds__(256) void gemm_fp8_join_kernel(const float* __restr
   else static_cast<unsigned short*>(C)[m * ldc + n] = (unsigned short)bf16_bits_rne(s);
 }
 
+// ---- few rows of A ----------------------------------------------------------------
+//
+// Up to 16 MT rows (MT 1 or 2): the weight's bytes are the work, and what counts is how many of them are
+// on their way.  One workgroup owns 16 columns and all of K, its 8 waves every eighth k block
+// of them, straight from memory into the operand registers (no LDS, no stages): 256
+// workgroups hold 4,096 columns, each wave some 8 KB in flight.  The waves' sums meet in LDS
+// and are added in wave order; there is no second launch and no workspace.
+
+constexpr int kFewWaves = 8;
+
+template <int MT, bool WIDE, bool E8M0, bool B_ROWS>
+__device__ __forceinline__ void gemm_fp8_few_rows(const GemmFp8KArgs& a) {
+  constexpr int U = 4;  // k blocks in flight
+  __shared__ f32x4 part[kFewWaves][MT][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lrow = lane & 15, lk = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const int nb = min(n0 + lrow, a.N - 1);
+  const uint8_t* b = a.B + (int64_t)nb * a.ldb + 16 * lk;
+  const uint8_t* ap[MT];
+  int ma[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    ma[i] = min(i * 16 + lrow, a.M - 1);
+    ap[i] = a.A + (int64_t)ma[i] * a.lda + 16 * lk;
+  }
+  auto scale_at = [&](const void* base, int64_t at) -> uint32_t {
+    return E8M0 ? (uint32_t) static_cast<const uint8_t*>(base)[at] : static_cast<const uint32_t*>(base)[at];
+  };
+  auto codes = [](const uint8_t* p) -> i32x8 {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(p), hi = *reinterpret_cast<const i32x4*>(p + 64);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  f32x4 acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = f32x4{};
+  for (int k0 = wave; k0 < a.KB; k0 += kFewWaves * U) {
+    i32x8 fb[U], fa[U][MT];
+    uint32_t sb[U][4], sa[U][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = min(k0 + u * kFewWaves, a.KB - 1);  // past the end: loaded, not used
+      fb[u] = codes(b + (int64_t)kb * 128);
+      if (E8M0) {
+        sb[u][0] = scale_at(a.sb, (int64_t)kb * a.sb_ld + (nb >> a.b_shift));
+      } else {
+#pragma unroll
+        for (int v = 0; v < (B_ROWS ? 4 : 1); ++v)
+          sb[u][v] = scale_at(a.sb, (int64_t)kb * a.sb_ld + (min(n0 + 4 * lk + v, a.N - 1) >> a.b_shift));
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        fa[u][i] = codes(ap[i] + (int64_t)kb * 128);
+        sa[u][i] = scale_at(a.sa, (int64_t)kb * a.M + ma[i]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k0 + u * kFewWaves >= a.KB) continue;  // uniform
+      bf16x8 wb[4], wa[4];
+      if (WIDE) widen_codes(fb[u], E8M0 ? e8m0_value(sb[u][0]) : 1.0f, wb);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        if (WIDE) widen_codes(fa[u][i], E8M0 ? e8m0_value(sa[u][i]) : 1.0f, wa);
+        f32x4 p = E8M0 ? acc[i] : f32x4{};
+        if (WIDE) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[q], wa[q], p, 0, 0, 0);
+        } else if (E8M0) {
+          p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[u], fa[u][i], p, 0, 0, 0, (int)sb[u][0], 0, (int)sa[u][i]);
+        } else {
+          p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[u], fa[u][i], p, 0, 0, 0, 0, 0, 0);
+        }
+        if (E8M0) {
+          acc[i] = p;
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            acc[i][v] = fmaf(p[v], __uint_as_float(sa[u][i]) * __uint_as_float(sb[u][B_ROWS ? v : 0]), acc[i][v]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+  __syncthreads();
+  for (int t = tid; t < MT * 64; t += kFewWaves * 64) {
+    const int i = t >> 6, l = t & 63;
+    f32x4 s = part[0][i][l];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) s += part[w][i][l];
+    const int m = i * 16 + (l & 15), n = n0 + 4 * (l >> 4);
+    if (m >= a.M) continue;
+    const int64_t at = (int64_t)m * a.ldc + n;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (n + v < a.N) {
+        if (a.c_f32) static_cast<float*>(a.C)[at + v] = s[v];
+        else static_cast<unsigned short*>(a.C)[at + v] = (unsigned short)bf16_bits_rne(s[v]);
+      }
+  }
+}
+
+template <int MT, bool WIDE, bool E8M0, bool B_ROWS>
+__global__ __launch_bounds__(kFewWaves * 64) void gemm_fp8_few_kernel(GemmFp8KArgs a) {
+  gemm_fp8_few_rows<MT, WIDE, E8M0, B_ROWS>(a);
+}
+
+template <int MT, bool WIDE>
+static void gemm_fp8_few_kinds(const GemmFp8Args& g, const GemmFp8KArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((g.N + 15) / 16)), block(kFewWaves * 64);
+  if (g.e8m0) hipLaunchKernelGGL((gemm_fp8_few_kernel<MT, WIDE, true, false>), grid, block, 0, stream, a);
+  else if (g.b_block == 1) hipLaunchKernelGGL((gemm_fp8_few_kernel<MT, WIDE, false, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((gemm_fp8_few_kernel<MT, WIDE, false, false>), grid, block, 0, stream, a);
+}
+
+template <bool WIDE>
+static hipError_t gemm_fp8_few(const GemmFp8Args& g, const GemmFp8KArgs& a, hipStream_t stream) {
+  if (g.M <= 16) gemm_fp8_few_kinds<1, WIDE>(g, a, stream);
+  else gemm_fp8_few_kinds<2, WIDE>(g, a, stream);
+  return hipGetLastError();
+}
+
 struct GemmFp8Plan {
   int bm, splits;
 };
 
+// Up to this many rows the few-row kernel runs.  4,096 columns, K 6,144: 16 rows 9 us or less
+// (the host's time per call) against 16 with 128 x 128 tiles and K split over 8 workgroups,
+// 32 rows 14 against 16; at 64 rows both take 17, and at 128 it took 28 against 19.
+constexpr int64_t kFewRows = 32;
+
 static GemmFp8Plan gemm_fp8_plan(int64_t M, int64_t N, int64_t KB) {
   GemmFp8Plan p = {256, 1};
+  if (M <= kFewRows) return GemmFp8Plan{0, 1};
   const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
   if (big >= 192) return p;
   p.bm = 128;
@@ -356,7 +485,7 @@ hipError_t launch_gemm_fp8(const GemmFp8Args& g, hipStream_t stream) {
   (void)hipGetLastError();
   if (g.M == 0 || g.N == 0) return hipSuccess;
   const GemmFp8Plan p = gemm_fp8_plan(g.M, g.N, g.KB);
-  GemmFp8KArgs a;
+  GemmFp8KArgs a = {};
   a.A = g.A;
   a.B = g.B;
   a.sa = g.sa;
@@ -368,6 +497,12 @@ hipError_t launch_gemm_fp8(const GemmFp8Args& g, hipStream_t stream) {
   a.KB = g.KB;
   a.sb_ld = g.b_block == 1 ? g.N : (g.N + 127) / 128;
   a.b_shift = g.b_block == 1 ? 0 : 7;
+  if (p.bm == 0) {
+    a.C = g.C;
+    a.c_f32 = g.c_f32;
+    a.ldc = g.ldc;
+    return g.c_f32 ? gemm_fp8_few<true>(g, a, stream) : gemm_fp8_few<false>(g, a, stream);
+  }
   a.tiles_m = (g.M + p.bm - 1) / p.bm;
   a.tiles_n = (g.N + p.bm - 1) / p.bm;
   a.group_m = 4;

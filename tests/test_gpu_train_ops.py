@@ -415,7 +415,7 @@ def product(eng, a, sa, b, sb, out):
     return out
 
 
-PRODUCTS = [(1, 1, 128), (1, 4096, 6144), (2, 8, 256), (5, 130, 384), (16, 256, 1024), (17, 100, 2560), (63, 513, 640),
+PRODUCTS = [(1, 1, 128), (1, 4096, 6144), (2, 8, 256), (5, 130, 384), (16, 256, 1024), (33, 72, 1152), (32, 200, 4224), (17, 100, 2560), (63, 513, 640),
             (64, 1024, 768), (129, 257, 896), (256, 4096, 6144), (200, 2000, 128), (1000, 1032, 1920),
             (3000, 4096, 512), (2048, 6144, 256), (3333, 4104, 384), (65, 129, 19_584)]
 
@@ -492,12 +492,12 @@ def test_matmul_of_no_rows(eng):
 
 def test_matmul_refuses_a_small_workspace(eng):
     g = gen(13)
-    a, sa = operand(g, 16, 6144, False, 1)
+    a, sa = operand(g, 200, 6144, False, 1)
     b, sb = operand(g, 4096, 6144, False, 128)
     with pytest.raises(eng.EngramError):
-        eng.engram_fp8_matmul(a, sa, b, sb, torch.empty((16, 4096), device=DEV))
+        eng.engram_fp8_matmul(a, sa, b, sb, torch.empty((200, 4096), device=DEV))
     with pytest.raises(ValueError):
-        eng.engram_fp8_matmul(a, sa[:, :3].contiguous(), b, sb, torch.empty((16, 4096), device=DEV))
+        eng.engram_fp8_matmul(a, sa[:, :3].contiguous(), b, sb, torch.empty((200, 4096), device=DEV))
 
 
 # ---------------------------------------------------------------------------

@@ -109,13 +109,14 @@ def test_matmul_refuses(change, status):
 
 
 def test_matmul_workspace():
-    need = eng.engram_fp8_matmul_workspace(16, 4096, 6144)
-    assert need > 0  # few rows: K is split
-    assert call(lib.engram_fp8_matmul, MATMUL, M=16, N=4096, K=6144, a_ld=6144, b_ld=6144, c_ld=4096, work_bytes=need - 1) \
+    need = eng.engram_fp8_matmul_workspace(200, 4096, 6144)
+    assert need > 0  # too few tiles for the chip: K is split
+    assert call(lib.engram_fp8_matmul, MATMUL, M=200, N=4096, K=6144, a_ld=6144, b_ld=6144, c_ld=4096, work_bytes=need - 1) \
         == eng.ENGRAM_E_SCRATCH
-    assert call(lib.engram_fp8_matmul, MATMUL, M=16, N=4096, K=6144, a_ld=6144, b_ld=6144, c_ld=4096, work=None) == \
+    assert call(lib.engram_fp8_matmul, MATMUL, M=200, N=4096, K=6144, a_ld=6144, b_ld=6144, c_ld=4096, work=None) == \
         eng.ENGRAM_E_SCRATCH
     assert eng.engram_fp8_matmul_workspace(65_536, 4096, 6144) == 0
+    assert eng.engram_fp8_matmul_workspace(16, 4096, 6144) == 0  # a few rows need none
     assert eng.engram_fp8_matmul_workspace(0, 4096, 6144) == 0
     assert eng.engram_fp8_matmul_workspace(5, 7, 100) == eng.engram_fp8_matmul_workspace(5, 7, 128)
     with pytest.raises(eng.EngramError):
