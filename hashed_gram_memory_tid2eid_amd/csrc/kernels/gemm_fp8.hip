@@ -39,13 +39,42 @@ struct GemmFp8KArgs {
   const void* sa;
   const void* sb;
   void* C;
-  int64_t lda, ldb, ldc, c_split_stride;
+  int64_t lda, ldb, ldc;
   int32_t M, N, KB;
   int32_t sb_ld, b_shift;    // entries per k block of sb; 0 or 7: row n reads entry n >> b_shift
   int32_t tiles_m, tiles_n, group_m;
+  int32_t whole;             // tiles 0 .. whole - 1 run over all of K; the others in splits of it
   int32_t kb_per_split;
+  float* work;               // the splits' tiles: [split][tile - whole][BM][BN]
   int32_t c_f32, vec_store;
 };
+
+// What a workgroup computes: a tile over all of K, or one split of a tile (part: which of the
+// splits' tiles in the workspace; -1: none, the tile goes to C).
+struct GemmFp8Tile {
+  int m, n, split, part;
+};
+
+__device__ __forceinline__ GemmFp8Tile gemm_fp8_tile_of(const GemmFp8KArgs& a, int block) {
+  GemmFp8Tile o = {0, 0, 0, -1};
+  int tile = block;
+  if (block >= a.whole) {
+    const int rest = a.tiles_m * a.tiles_n - a.whole;
+    o.part = block - a.whole;
+    o.split = o.part / rest;
+    tile = a.whole + (o.part - o.split * rest);
+  } else if ((a.whole & 7) == 0) {  // each XCD takes a run of consecutive tiles
+    tile = (block & 7) * (a.whole >> 3) + (block >> 3);
+  }
+  const int group = a.group_m * a.tiles_n;
+  const int gid = tile / group;
+  const int first_m = gid * a.group_m;
+  const int gm = min(a.tiles_m - first_m, a.group_m);
+  const int in_group = tile - gid * group;
+  o.m = first_m + in_group % gm;
+  o.n = in_group / gm;
+  return o;
+}
 
 // A barrier that the compiler moves no memory access across (the builtin alone only stops
 // the hardware); the waits that make LDS contents visible are the caller's.
@@ -81,23 +110,10 @@ __device__ __forceinline__ void gemm_fp8_tile(const GemmFp8KArgs& a) {
   static_assert(128 % WN == 0, "a wave's columns share their 128-block");
   extern __shared__ __attribute__((aligned(1024))) char smem[];
 
-  const int ntiles = a.tiles_m * a.tiles_n;
-  int bid = blockIdx.x;
-  const int split = bid / ntiles;
-  bid -= split * ntiles;
-  if ((ntiles & 7) == 0) {
-    const int per_xcd = ntiles >> 3;
-    bid = (bid & 7) * per_xcd + (bid >> 3);
-  }
-  const int group = a.group_m * a.tiles_n;
-  const int gid = bid / group;
-  const int first_m = gid * a.group_m;
-  const int gm = min(a.tiles_m - first_m, a.group_m);
-  const int in_group = bid - gid * group;
-  const int m0 = (first_m + in_group % gm) * BM;
-  const int n0 = (in_group / gm) * BN;
-  const int kb0 = split * a.kb_per_split;
-  const int nk = min(a.kb_per_split, a.KB - kb0);
+  const GemmFp8Tile at = gemm_fp8_tile_of(a, blockIdx.x);
+  const int m0 = at.m * BM, n0 = at.n * BN;
+  const int kb0 = at.split * a.kb_per_split;
+  const int nk = at.part < 0 ? a.KB : min(a.kb_per_split, a.KB - kb0);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN_WAVES, wn = wave % WN_WAVES;
@@ -260,9 +276,19 @@ __device__ __forceinline__ void gemm_fp8_tile(const GemmFp8KArgs& a) {
   constexpr int PITCH = WN + 4;
   static_assert(NWAVES * 16 * PITCH * 4 <= 2 * STAGE, "the slabs fit in the ring");
   float* slab = reinterpret_cast<float*>(smem) + wave * 16 * PITCH;
-  const int64_t base = (int64_t)split * a.c_split_stride;
+  // the tile in C, or the split's in the workspace; where it is is worked out again, so that
+  // the loop need not hold it
+  int block = blockIdx.x;
+  asm volatile("" : "+s"(block));
+  const GemmFp8Tile to = gemm_fp8_tile_of(a, block);
+  const bool part = to.part >= 0;
+  void* const out = part ? (void*)(a.work + (int64_t)to.part * (BM * BN))
+                         : (void*)(static_cast<char*>(a.C) + ((int64_t)to.m * BM * a.ldc + to.n * BN) * (a.c_f32 ? 4 : 2));
+  const int left_m = a.M - to.m * BM, left_n = a.N - to.n * BN;
+  const int64_t ld = part ? BN : a.ldc;
+  const bool out_f32 = part || a.c_f32, vec = part || a.vec_store;
   constexpr int LANES = WN / 4, ROWS = 64 / LANES;  // lanes per row, rows per pass
-  const int n = n0 + wn * WN + (lane % LANES) * 4;
+  const int n = wn * WN + (lane % LANES) * 4;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
 #pragma unroll
@@ -272,24 +298,24 @@ __device__ __forceinline__ void gemm_fp8_tile(const GemmFp8KArgs& a) {
     for (int q = 0; q < 16 / ROWS; ++q) {
       const int r = q * ROWS + lane / LANES;
       const f32x4 val = *reinterpret_cast<const f32x4*>(slab + r * PITCH + (lane % LANES) * 4);
-      const int m = m0 + wm * WM + i * 16 + r;
-      if (m >= a.M || n >= a.N) continue;
-      const int64_t at = base + (int64_t)m * a.ldc + n;
-      if (a.vec_store && n + 4 <= a.N) {
-        if (a.c_f32) {
-          *reinterpret_cast<f32x4*>(static_cast<float*>(a.C) + at) = val;
+      const int m = wm * WM + i * 16 + r;
+      if (m >= left_m || n >= left_n) continue;
+      const int64_t at = (int64_t)m * ld + n;
+      if (vec && n + 4 <= left_n) {
+        if (out_f32) {
+          *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) = val;
         } else {
           uint2 o;
           o.x = bf16_bits_rne(val[0]) | (bf16_bits_rne(val[1]) << 16);
           o.y = bf16_bits_rne(val[2]) | (bf16_bits_rne(val[3]) << 16);
-          *reinterpret_cast<uint2*>(static_cast<unsigned short*>(a.C) + at) = o;
+          *reinterpret_cast<uint2*>(static_cast<unsigned short*>(out) + at) = o;
         }
       } else {
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-          if (n + v < a.N) {
-            if (a.c_f32) static_cast<float*>(a.C)[at + v] = val[v];
-            else static_cast<unsigned short*>(a.C)[at + v] = (unsigned short)bf16_bits_rne(val[v]);
+          if (n + v < left_n) {
+            if (out_f32) static_cast<float*>(out)[at + v] = val[v];
+            else static_cast<unsigned short*>(out)[at + v] = (unsigned short)bf16_bits_rne(val[v]);
           }
       }
     }
@@ -302,16 +328,26 @@ __global__ __launch_bounds__(WM_WAVES* WN_WAVES * 64) void gemm_fp8_kernel(GemmF
   gemm_fp8_tile<BM, BN, WM_WAVES, WN_WAVES, WIDE, E8M0, B_ROWS>(a);
 }
 
-// C = the sum of the split-K slices, in slice order
-__global__ __launch_bounds__(256) void gemm_fp8_join_kernel(const float* __restrict__ work, int32_t splits, int64_t MN,
-                                                            int32_t N, void* C, int32_t c_f32, int64_t ldc) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= MN) return;
-  float s = work[i];
-  for (int p = 1; p < splits; ++p) s += work[(int64_t)p * MN + i];
-  const int64_t m = i / N, n = i - m * N;
-  if (c_f32) static_cast<float*>(C)[m * ldc + n] = s;
-  else static_cast<unsigned short*>(C)[m * ldc + n] = (unsigned short)bf16_bits_rne(s);
+// The tiles whose K was split: C = the sum of their splits, in order.  A workgroup joins 1,024
+// elements of one tile, 4 a thread.
+template <int BM>
+__global__ __launch_bounds__(256) void gemm_fp8_join_kernel(GemmFp8KArgs a, int32_t splits) {
+  constexpr int PER = BM * BM / 1024;
+  const int rest = a.tiles_m * a.tiles_n - a.whole;
+  const int t = blockIdx.x / PER, e = (blockIdx.x % PER) * 1024 + threadIdx.x * 4;
+  const GemmFp8Tile tile = gemm_fp8_tile_of(a, a.whole + t);
+  const int m = tile.m * BM + e / BM, n = tile.n * BM + e % BM;
+  if (m >= a.M || n >= a.N) return;
+  const float* w = a.work + (int64_t)t * (BM * BM) + e;
+  f32x4 s = *reinterpret_cast<const f32x4*>(w);
+  for (int p = 1; p < splits; ++p) s += *reinterpret_cast<const f32x4*>(w + (int64_t)p * rest * (BM * BM));
+  const int64_t at = (int64_t)m * a.ldc + n;
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (n + v < a.N) {
+      if (a.c_f32) static_cast<float*>(a.C)[at + v] = s[v];
+      else static_cast<unsigned short*>(a.C)[at + v] = (unsigned short)bf16_bits_rne(s[v]);
+    }
 }
 
 // ---- few rows of A ----------------------------------------------------------------
@@ -438,7 +474,10 @@ static hipError_t gemm_fp8_few(const GemmFp8Args& g, const GemmFp8KArgs& a, hipS
 }
 
 struct GemmFp8Plan {
-  int bm, splits;
+  int bm;             // 256 or 128 (square tiles), 0: the few-row kernel
+  int64_t whole;      // tiles that run over all of K
+  int64_t rest;       // tiles whose K is split
+  int splits;
 };
 
 // Up to this many rows the few-row kernel runs.  4,096 columns, K 6,144: 16 rows 9 us or less
@@ -446,20 +485,42 @@ struct GemmFp8Plan {
 // 32 rows 14 against 16; at 64 rows both take 17, and at 128 it took 28 against 19.
 constexpr int64_t kFewRows = 32;
 
+// 256 x 256 tiles, one workgroup per CU, from 192 of them on; the tiles of a last, partly
+// filled round are split over K, so that they fill it (4,096 x 6,144 over 16,384, 384 tiles:
+// 656 -> 563 us with e8m0 scales).  Fewer tiles are 128 x 128, all of them split while there is a workgroup for
+// every CU and two k blocks for each split.
 static GemmFp8Plan gemm_fp8_plan(int64_t M, int64_t N, int64_t KB) {
-  GemmFp8Plan p = {256, 1};
-  if (M <= kFewRows) return GemmFp8Plan{0, 1};
-  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
-  if (big >= 192) return p;
-  p.bm = 128;
-  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
-  while (tiles * p.splits * 2 <= 256 && KB / (p.splits * 2) >= 2) p.splits *= 2;
+  GemmFp8Plan p = {0, 0, 0, 1};
+  if (M <= kFewRows) return p;
+  int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  if (tiles >= 192) {
+    p.bm = 256;
+    p.rest = tiles > 256 ? tiles % 256 : 0;
+    const int64_t s = p.rest > 0 ? 256 / p.rest : 1;
+    // at least 8 k blocks to a split: a split's tile costs a write and a read of its sums
+    p.splits = (int)(s < KB / 8 ? s : KB / 8);
+    if (p.splits > 8) p.splits = 8;
+  } else {
+    p.bm = 128;
+    tiles = ((M + 127) / 128) * ((N + 127) / 128);
+    p.rest = tiles;
+    while (tiles * p.splits * 2 <= 256 && KB / (p.splits * 2) >= 2) p.splits *= 2;
+  }
+  if (p.splits > 1) {  // every split has work
+    const int64_t per = (KB + p.splits - 1) / p.splits;
+    p.splits = (int)((KB + per - 1) / per);
+  }
+  if (p.splits <= 1) {
+    p.splits = 1;
+    p.rest = 0;
+  }
+  p.whole = tiles - p.rest;
   return p;
 }
 
 int64_t gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t KB) {
   const GemmFp8Plan p = gemm_fp8_plan(M, N, KB);
-  return p.splits > 1 ? (int64_t)p.splits * M * N * 4 : 0;
+  return p.rest * p.splits * p.bm * p.bm * 4;
 }
 
 template <int BM, int WM_WAVES, int WN_WAVES, bool WIDE, bool E8M0, bool B_ROWS>
@@ -497,34 +558,30 @@ hipError_t launch_gemm_fp8(const GemmFp8Args& g, hipStream_t stream) {
   a.KB = g.KB;
   a.sb_ld = g.b_block == 1 ? g.N : (g.N + 127) / 128;
   a.b_shift = g.b_block == 1 ? 0 : 7;
-  if (p.bm == 0) {
-    a.C = g.C;
-    a.c_f32 = g.c_f32;
-    a.ldc = g.ldc;
-    return g.c_f32 ? gemm_fp8_few<true>(g, a, stream) : gemm_fp8_few<false>(g, a, stream);
-  }
+  a.C = g.C;
+  a.c_f32 = g.c_f32;
+  a.ldc = g.ldc;
+  if (p.bm == 0) return g.c_f32 ? gemm_fp8_few<true>(g, a, stream) : gemm_fp8_few<false>(g, a, stream);
   a.tiles_m = (g.M + p.bm - 1) / p.bm;
   a.tiles_n = (g.N + p.bm - 1) / p.bm;
   a.group_m = 4;
+  a.whole = (int32_t)p.whole;
   a.kb_per_split = (g.KB + p.splits - 1) / p.splits;
-  const int splits = (g.KB + a.kb_per_split - 1) / a.kb_per_split;  // every split has work
-  const bool joined = splits > 1;
-  a.C = joined ? (void*)g.work : g.C;
-  a.c_f32 = joined ? 1 : g.c_f32;
-  a.ldc = joined ? g.N : g.ldc;
-  a.c_split_stride = joined ? (int64_t)g.M * g.N : 0;
-  a.vec_store = (a.ldc % 4 == 0 && a.c_split_stride % 4 == 0 && ((uintptr_t)a.C & 15) == 0) ? 1 : 0;
-  const int64_t grid = (int64_t)a.tiles_m * a.tiles_n * splits;
+  a.work = g.work;
+  a.vec_store = (a.ldc % 4 == 0 && ((uintptr_t)a.C & 15) == 0) ? 1 : 0;
+  const int64_t grid = p.whole + p.rest * p.splits;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipError_t e;
   if (p.bm == 256)
     e = g.c_f32 ? gemm_fp8_kinds<256, 2, 4, true>(g, a, grid, stream) : gemm_fp8_kinds<256, 2, 4, false>(g, a, grid, stream);
   else
     e = g.c_f32 ? gemm_fp8_kinds<128, 2, 2, true>(g, a, grid, stream) : gemm_fp8_kinds<128, 2, 2, false>(g, a, grid, stream);
-  if (e != hipSuccess || !joined) return e;
-  const int64_t MN = (int64_t)g.M * g.N;
-  hipLaunchKernelGGL(gemm_fp8_join_kernel, dim3((unsigned)((MN + 255) / 256)), dim3(256), 0, stream, g.work, splits, MN,
-                     g.N, g.C, g.c_f32, g.ldc);
+  if (e != hipSuccess || p.rest == 0) return e;
+  const int64_t joins = p.rest * (p.bm * p.bm / 1024);
+  if (p.bm == 256)
+    hipLaunchKernelGGL((gemm_fp8_join_kernel<256>), dim3((unsigned)joins), dim3(256), 0, stream, a, p.splits);
+  else
+    hipLaunchKernelGGL((gemm_fp8_join_kernel<128>), dim3((unsigned)joins), dim3(256), 0, stream, a, p.splits);
   return hipGetLastError();
 }
 

@@ -417,7 +417,7 @@ def product(eng, a, sa, b, sb, out):
 
 PRODUCTS = [(1, 1, 128), (1, 4096, 6144), (2, 8, 256), (5, 130, 384), (16, 256, 1024), (33, 72, 1152), (32, 200, 4224), (17, 100, 2560), (63, 513, 640),
             (64, 1024, 768), (129, 257, 896), (256, 4096, 6144), (200, 2000, 128), (1000, 1032, 1920),
-            (3000, 4096, 512), (2048, 6144, 256), (3333, 4104, 384), (65, 129, 19_584)]
+            (3000, 4096, 512), (2048, 6144, 256), (3333, 4104, 384), (5000, 4104, 2176), (65, 129, 19_584)]
 
 
 @pytest.mark.parametrize("M, N, K", PRODUCTS)
