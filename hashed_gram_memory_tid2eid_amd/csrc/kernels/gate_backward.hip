@@ -117,7 +117,7 @@ __global__ __launch_bounds__(THREADS) void gate_backward_kernel(GateBackwardArgs
         dv[h][i0] = fmaf(g[s], dlo, fmaf(e[s], bf16_lo(x[s][c][w]), dv[h][i0]));
         dv[h][i1] = fmaf(g[s], dhi, fmaf(e[s], bf16_hi(x[s][c][w]), dv[h][i1]));
       }
-      *reinterpret_cast<g_u32x4*>(dxrow + (int64_t)s * a.hidden + ch * 8) = o;
+      __builtin_nontemporal_store(o, reinterpret_cast<g_u32x4*>(dxrow + (int64_t)s * a.hidden + ch * 8));
     }
     *reinterpret_cast<g_f32x4*>(dvrow + ch * 8) = dv[0];
     *reinterpret_cast<g_f32x4*>(dvrow + ch * 8 + 4) = dv[1];

@@ -174,7 +174,7 @@ __global__ __launch_bounds__(kQuantThreads) void fp8_quantize_kernel(QuantKArgs 
       uint2 o;
       o.x = pack_e4m3x4(y[0], y[1], y[2], y[3]);
       o.y = pack_e4m3x4(y[4], y[5], y[6], y[7]);
-      *reinterpret_cast<uint2*>(a.q + m * a.q_ld + k0) = o;
+      __builtin_nontemporal_store((uint64_t)o.x | ((uint64_t)o.y << 32), reinterpret_cast<uint64_t*>(a.q + m * a.q_ld + k0));
     }
   }
 
@@ -205,10 +205,9 @@ __global__ __launch_bounds__(kQuantThreads) void fp8_quantize_kernel(QuantKArgs 
       const int col = p * 32 + (tid >> 3), part = tid & 7;
       const int64_t k = (int64_t)kb * 128 + col;
       if (k >= a.K) continue;
-      ulonglong2 o;
-      o.x = tile[quant_slot(col, 2 * part)];
-      o.y = tile[quant_slot(col, 2 * part + 1)];
-      *reinterpret_cast<ulonglong2*>(a.qt + k * a.qt_ld + m0 + part * 16) = o;
+      const uint64_t lo = tile[quant_slot(col, 2 * part)], hi = tile[quant_slot(col, 2 * part + 1)];
+      const u32x4 o = {(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+      __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(a.qt + k * a.qt_ld + m0 + part * 16));
     }
   }
 }
