@@ -222,6 +222,38 @@ def test_embed_grad_long_runs(eng, n, kind):
     assert torch.equal(unique[:count].long(), torch.nonzero(terms).flatten())
 
 
+@pytest.mark.parametrize("n", [1, 63, 1023, 1024, 1025, 4096, 4097, 8192, 8193, 16_383, 16_384, 16_385])
+@pytest.mark.parametrize("rows", [1 << 27, 1 << 28, 384_006_168, 2**31 - 1])
+def test_embed_grad_names_rows_of_large_tables(eng, n, rows):
+    """Ids of 28 to 31 bits, short lists and long ones: every id once by name, its places added in
+    their order.  Whole numbers: sums are exact."""
+    g = gen(n)
+    pool = torch.randint(0, rows, (n // 2 + 1,), generator=g, device=DEV)
+    pool[0] = rows - 1
+    ids = pool[torch.randint(0, pool.numel(), (n, 1), generator=g, device=DEV)].int()
+    dout = torch.randint(-4, 5, (n, 16), generator=g, device=DEV).to(BF16)
+    grad, unique, count = run_grad(eng, ids, dout, rows, 16, 16, 1.0, "sparse", F32)
+    names, inverse = torch.unique(ids.flatten().long(), return_inverse=True)
+    assert count == names.numel() and torch.equal(unique[:count].long(), names)
+    assert bool((unique[count:] == -1).all())
+    ref = torch.zeros((count, 16), dtype=torch.float64, device=DEV).index_add_(0, inverse, dout.double())
+    assert torch.equal(grad[:count].double(), ref)
+
+
+@pytest.mark.parametrize("n, rows", [(1, 3), (256, 257), (3000, 12_288), (20_000, 300), (20_000, 70_000)])
+@pytest.mark.parametrize("hot", [False, True])
+def test_embed_grad_dense_writes_every_row_once(eng, n, rows, hot):
+    """Rows without a place are zero, whether a part of the list around them is short or holds
+    most of it (one row's places)."""
+    g = gen(rows)
+    ids = torch.randint(0, rows, (n, 1), generator=g, device=DEV, dtype=torch.int32)
+    if hot:
+        ids[torch.rand((n, 1), generator=g, device=DEV) < 0.8] = rows // 2
+    dout = torch.randint(-4, 5, (n, 64), generator=g, device=DEV).to(BF16)
+    ref, _, _ = grad_ref(ids, dout, rows, 64, 64, 1.0)
+    assert torch.equal(run_grad(eng, ids, dout, rows, 64, 64, 1.0, "dense", F32).double(), ref)
+
+
 def test_embed_grad_repeats_bit_for_bit_and_ignores_the_workspace(eng):
     g = gen(5)
     ids = torch.randint(0, 40, (3000, 2), generator=g, device=DEV, dtype=torch.int32)
