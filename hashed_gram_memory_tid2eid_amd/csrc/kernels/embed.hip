@@ -12,9 +12,12 @@
 // consecutive lanes take consecutive chunks, so a wave's loads and stores are runs of whole
 // cache lines.  Each lane first fetches the ids of its UNROLL chunks, then all their table
 // bytes, then stores: that many independent row reads are in flight per lane.  Large calls
-// write past the caches, which then keep table rows instead: 65,536 x 24 rows of 256 bf16
-// (Zipf ids, 4M rows) 172 us against 289 with ordinary stores (805 MB written), fp32 output
-// 290 against 490.  With 2 or 1 chunks in flight 176 and 190 us, with 8 (registers) 224.
+// write past the caches, which then keep table rows instead.  65,536 x 24 rows of 256 bf16
+// (Zipf ids, 4M rows, 805 MB written and some 140 MB of distinct rows): 157 us where the rows
+// are in the last cache (with ordinary stores 272), 246 us where they come from memory; fp32
+// output 264 (464) and 421.  Uniform ids read as much as they write, 1.6 GB in 266 us, 6.1 TB/s:
+// it is memory's rate for single rows between the writes that bounds it.  In the order 8, 2, 1
+// chunks in flight 259, 257, 304 us from memory; rows read past the caches 282.
 
 namespace engram {
 
@@ -107,42 +110,77 @@ __device__ __forceinline__ void store_chunk(void* base, int64_t e, int n, bool v
   }
 }
 
+// N elements of a table row as they are loaded, and as floats
+template <bool F32, int N>
+struct RowChunk {
+  static constexpr int WORDS = F32 ? N : N / 2;
+  uint32_t w[WORDS];
+  __device__ __forceinline__ void load(const void* base, int64_t e, int n, bool vec) {
+    if (vec && n == N) {
+      typedef uint32_t words __attribute__((ext_vector_type(WORDS < 4 ? WORDS : 4)));
+      constexpr int PER = WORDS < 4 ? WORDS : 4;
+      const words* src = reinterpret_cast<const words*>(static_cast<const char*>(base) + e * (F32 ? 4 : 2));
+#pragma unroll
+      for (int h = 0; h < WORDS / PER; ++h) {
+        const words v = src[h];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) w[PER * h + i] = v[i];
+      }
+    } else {
+      float f[N];
+      load_chunk<F32, N>(base, e, n, false, f);
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i)
+        w[i] = F32 ? __float_as_uint(f[F32 ? i : 0])
+                   : (__float_as_uint(f[F32 ? 0 : 2 * i]) >> 16) | __float_as_uint(f[F32 ? 0 : 2 * i + 1]);
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if (F32) return __uint_as_float(w[F32 ? i : 0]);
+    const uint32_t v = w[F32 ? 0 : i / 2];
+    return __uint_as_float(i % 2 ? v & 0xFFFF0000u : v << 16);
+  }
+};
+
 template <bool TABLE_F32, bool OUT_F32, int UNROLL>
 __global__ __launch_bounds__(kEmbedThreads) void embed_kernel(EmbedKArgs a) {
   constexpr int N = OUT_F32 ? 4 : 8;  // elements per chunk
   const uint32_t first = blockIdx.x * (kEmbedThreads * UNROLL) + threadIdx.x;
-  float f[UNROLL][N];
-  int64_t dst[UNROLL];
-  int n[UNROLL];
+  // all ids, then all rows: a wait for an id that was asked for behind a row waits for the row, too
+  int32_t row[UNROLL];
 #pragma unroll
   for (int u = 0; u < UNROLL; ++u) {
-    const uint32_t g = first + (uint32_t)u * kEmbedThreads;
-    n[u] = 0;
-    dst[u] = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[u][i] = 0.0f;
-    if (g >= a.total) continue;
-    const uint32_t seg = fdiv(g, a.div_chunks);  // token * cols + column
-    const uint32_t chunk = g - seg * a.chunks;
+    const uint32_t seg = fdiv(min(first + (uint32_t)u * kEmbedThreads, a.total - 1), a.div_chunks);  // token * cols + column
     const uint32_t t = fdiv(seg, a.div_cols);
-    const uint32_t c = seg - t * a.cols;
-    const int e0 = (int)chunk * N;
-    n[u] = (int)min((int64_t)N, a.seg_pitch - e0);
-    dst[u] = (int64_t)t * a.out_ld + (int64_t)c * a.seg_pitch + e0;
-    const int32_t row = a.ids[(int64_t)t * a.ids_ld + c];
-    if (row < 0 || row >= a.rows) {
-      if (row != -1) latch_error(ENGRAM_E_ROW_RANGE);
-      continue;
+    row[u] = a.ids[(int64_t)t * a.ids_ld + (seg - t * a.cols)];
+  }
+  RowChunk<TABLE_F32, N> raw[UNROLL];
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    const uint32_t g = min(first + (uint32_t)u * kEmbedThreads, a.total - 1);
+    const int e0 = (int)(g - fdiv(g, a.div_chunks) * a.chunks) * N;
+    raw[u].clear();
+    if (row[u] < 0 || row[u] >= a.rows) {
+      if (row[u] != -1) latch_error(ENGRAM_E_ROW_RANGE);
+    } else if (e0 < a.dim) {
+      raw[u].load(a.table, (int64_t)row[u] * a.table_ld + e0, min(N, a.dim - e0), a.table_vec != 0);
     }
-    if (e0 >= a.dim) continue;
-    load_chunk<TABLE_F32, N>(a.table, (int64_t)row * a.table_ld + e0, min(N, a.dim - e0), a.table_vec != 0, f[u]);
   }
 #pragma unroll
   for (int u = 0; u < UNROLL; ++u) {
-    if (n[u] == 0) continue;
+    const uint32_t g = first + (uint32_t)u * kEmbedThreads;
+    if (g >= a.total) continue;
+    const uint32_t seg = fdiv(g, a.div_chunks), t = fdiv(seg, a.div_cols);
+    const int e0 = (int)(g - seg * a.chunks) * N;
+    float f[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[u][i] *= a.scale;
-    store_chunk<OUT_F32, N, (UNROLL > 1)>(a.out, dst[u], n[u], a.out_vec != 0, f[u]);
+    for (int i = 0; i < N; ++i) f[i] = raw[u].at(i) * a.scale;
+    store_chunk<OUT_F32, N, (UNROLL > 1)>(a.out, (int64_t)t * a.out_ld + (int64_t)(seg - t * a.cols) * a.seg_pitch + e0,
+                                          (int)min((int64_t)N, a.seg_pitch - e0), a.out_vec != 0, f);
   }
 }
 
