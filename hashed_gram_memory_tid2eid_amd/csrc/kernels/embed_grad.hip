@@ -4,13 +4,12 @@
 //   grad[r][d] = scale * sum over the places (t, c) with ids[t][c] = r of dout[t][c seg_pitch + d]
 //
 // The places are sorted by row id, stably (id -1 and ids outside the table sort behind every
-// row), so a row's places are one run.  Up to kSmallSort places each finds its place in the
-// sorted list by counting, in one launch; more take a radix sort over as many bits as the
-// table's row count has, three launches for each digit of up to 10 bits.  The zeros of a dense gradient's other rows
-// are written by workgroups beside those that sum, which find by a search of the sorted list
-// which rows those are, so that every row is written once.  Only a large gradient (over 64 MB)
-// of a short list is cleared whole, beside its sort, which otherwise leaves the chip idle:
-// 16,384 tokens, 129,280 x 4,096 fp32 437 us against 452; long lists 344 us against 307.
+// row), so a row's places are one run.  Up to kMergeSort places each finds its place in the
+// sorted list by counting, in one launch or two; more take a radix sort over as many bits as
+// the table's row count has, three launches for each digit of up to 10 bits.  The zeros of a
+// dense gradient's other rows are written by workgroups beside those that sum, which find in the sorted list which rows
+// those are, so that every row is written once (16,384 tokens, 129,280 x 4,096 fp32: 435 us,
+// 5.2 TB/s; cleared whole beside the sort 475).
 //
 // The sorted list is cut into chunks of `ch` places; a group of lanes owns one chunk and one
 // range of columns, 8 per lane (two runs of 4, so that fp32 rows are read and written in
@@ -27,9 +26,9 @@ namespace engram {
 // (16 waves of 2 places a lane: 393,216 places in 4 waves of 8 took 11 us longer)
 constexpr int kSortThreads = 1024, kSortItems = 2, kSortTile = kSortThreads * kSortItems;
 constexpr int kSortBits = 10;     // digit of the sort over many workgroups
-constexpr int kSmallThreads = 1024, kSmallItems = 16, kSmallSort = kSmallThreads * kSmallItems;
-constexpr int kZeroBlocks = 255;  // workgroups beside it that clear a large dense gradient: one per other CU
-constexpr int64_t kZeroFirst = 64 << 20;  // bytes above which they do
+constexpr int kSmallThreads = 1024;
+constexpr int kCountSort = 4096;  // up to this many places are ranked by counting,
+constexpr int kMergeTile = 256, kMergeSort = 32768;  // up to this many by tiles
 constexpr int kSegThreads = 256;
 constexpr int kUnit = 32;         // chunks per unit
 constexpr int kFewUnits = 16;     // up to this many units, runs add their heads without unit sums
@@ -247,43 +246,17 @@ __global__ __launch_bounds__(256) void run_scan_kernel(RunKArgs a) {
   if (threadIdx.x == 0) *a.count = (int32_t)carry;
 }
 
-// ---- the zeros of a large dense gradient of a short list ----------------------------------
-
-// Workgroup `block` of `blocks` walks memory in step with the others, so that the chip writes
-// one window of consecutive lines at a time.
-template <int THREADS>
-__device__ __forceinline__ void zero_memory(char* base, int64_t bytes, uint32_t block, uint32_t blocks) {
-  constexpr int U = 4;
-  const u32x4 zero = {};
-  u32x4* p = reinterpret_cast<u32x4*>(base);
-  const int64_t words = bytes / 16, step = (int64_t)blocks * THREADS * U;
-  int64_t i = (int64_t)block * THREADS * U + threadIdx.x;
-  for (; i + (U - 1) * THREADS < words; i += step) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) p[i + u * THREADS] = zero;
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (i + u * THREADS < words) p[i + u * THREADS] = zero;
-  if (block == 0 && (int64_t)threadIdx.x < bytes - words * 16) base[words * 16 + threadIdx.x] = 0;
-}
-
 // ---- a short list: sorted by one workgroup, in LDS -------------------------------------
 
 // Rank of a place = the places with a smaller key, and those before it with the same.  Each
 // workgroup holds all keys in LDS and ranks 64 / SPLIT places: SPLIT lanes of every wave count
 // for one place over equal shares of the list, a compare and an add with carry a pair.  The
 // whole gradient of 12,288 rows of 128 with this or with a sort by digits in one workgroup: 1
-// place 8 us against 15, 3,000 places 17 against 25, 16,384 places 39 against 49.
+// place 8 us against 15, 3,000 places 17 against 25.
 template <int SPLIT>
-__global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortKArgs a, char* zero, int64_t zero_bytes) {
+__global__ __launch_bounds__(kSmallThreads) void sort_count_all_kernel(SortKArgs a) {
   constexpr uint32_t PLACES = 64 / SPLIT, SHARES = kSmallThreads / PLACES;
-  const uint32_t sorters = (a.n + PLACES - 1) / PLACES;
-  if (blockIdx.x >= sorters) {
-    zero_memory<kSmallThreads>(zero, zero_bytes, blockIdx.x - sorters, gridDim.x - sorters);
-    return;
-  }
-  __shared__ __attribute__((aligned(16))) uint32_t keys[kSmallSort];
+  __shared__ __attribute__((aligned(16))) uint32_t keys[kCountSort];
   // (one address a wave where the shares are the waves')
   const uint32_t tid = threadIdx.x, lane = tid % PLACES;
   const uint32_t part = SPLIT == 1 ? (uint32_t)__builtin_amdgcn_readfirstlane(tid / PLACES) : tid / PLACES;
@@ -321,37 +294,104 @@ __global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SortKArgs a, 
 }
 
 template <int SPLIT>
-static void launch_sort_small(const SortKArgs& s, char* zero, int64_t zero_bytes, hipStream_t stream) {
-  const unsigned sorters = (s.n * SPLIT + 63) / 64;
-  if (sorters == 0) return;
-  hipLaunchKernelGGL((sort_small_kernel<SPLIT>), dim3(sorters + (zero_bytes > 0 ? kZeroBlocks : 0)), dim3(kSmallThreads), 0,
-                     stream, s, zero, zero_bytes);
+static void launch_count_all(const SortKArgs& s, hipStream_t stream) {
+  const unsigned grid = (s.n * SPLIT + 63) / 64;
+  if (grid > 0) hipLaunchKernelGGL((sort_count_all_kernel<SPLIT>), dim3(grid), dim3(kSmallThreads), 0, stream, s);
 }
 
-// the runs of a short list, in one workgroup
-__global__ __launch_bounds__(kSmallThreads) void run_small_kernel(RunKArgs r) {
-  __shared__ uint32_t wsum[kSmallThreads / 64];
-  // a thread's `span` consecutive places, whole chunks of 4
-  const uint32_t span = (r.n + kSmallThreads * 4 - 1) / (kSmallThreads * 4) * 4, tid = threadIdx.x;
-  const uint32_t s0 = tid * span;
-  uint32_t starts = 0, c = 0;
-  uint32_t last = s0 > 0 && s0 < r.n ? r.key[s0 - 1] : r.rows;
+// Longer lists: each workgroup sorts a tile by counting, then every place is looked up in every
+// tile.  A workgroup holds all tiles in LDS and ranks 64 places of one tile, a lane each; its
+// waves take the tiles in turn.  16,384 places: 5 + 5 us; all pairs counted 29 us, which is the time
+// to read the keys from LDS once per workgroup.
+__global__ __launch_bounds__(kSmallThreads) void sort_tile_kernel(SortKArgs a) {
+  constexpr uint32_t SHARES = kSmallThreads / kMergeTile, SHARE = kMergeTile / SHARES;  // waves per place; places a wave looks at
+  static_assert(SHARE == 64, "a wave's places are one share");
+  __shared__ __attribute__((aligned(16))) uint32_t keys[kMergeTile];
+  __shared__ uint32_t counts[SHARES][kMergeTile];
+  const uint32_t tid = threadIdx.x, p = tid % kMergeTile, at = blockIdx.x * kMergeTile + p;
+  const uint32_t mine = (uint32_t)__builtin_amdgcn_readfirstlane(p / SHARE);
+  const uint32_t share = (uint32_t)__builtin_amdgcn_readfirstlane(tid / kMergeTile);
+  if (tid < kMergeTile) keys[tid] = at < a.n ? place_key<true>(a, at) : 0xFFFFFFFFu;
+  __syncthreads();
+  const uint32_t key = keys[p], *from = keys + share * SHARE;
+  uint32_t below = 0;
+  if (share == mine) {
+#pragma unroll 16
+    for (uint32_t j = 0; j < SHARE; ++j) below += from[j] < key + (j < p % SHARE ? 1u : 0u) ? 1u : 0u;
+  } else {
+    const uint32_t limit = key + (share < mine ? 1u : 0u);
+#pragma unroll 16
+    for (uint32_t j = 0; j < SHARE; ++j) below += from[j] < limit ? 1u : 0u;
+  }
+  counts[share][p] = below;
+  __syncthreads();
+  if (tid >= kMergeTile || at >= a.n) return;
+  uint32_t rank = blockIdx.x * kMergeTile;
 #pragma unroll
-  for (uint32_t e = 0; e < kSmallSort / kSmallThreads; ++e) {
-    if (e >= span || s0 + e >= r.n) continue;
-    const uint32_t k = r.key[s0 + e];
-    if (k < r.rows && k != last) {
-      starts |= 1u << e;
-      ++c;
+  for (uint32_t e = 0; e < SHARES; ++e) rank += counts[e][p];
+  a.key_out[rank] = key;
+  a.pos_out[rank] = at;
+}
+
+__global__ __launch_bounds__(kSmallThreads) void sort_merge_kernel(SortKArgs a) {
+  constexpr uint32_t WAVES = kSmallThreads / 64;
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem);  // whole tiles
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = (uint32_t)__builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t tiles = (a.n + kMergeTile - 1) / kMergeTile;
+  for (uint32_t i = tid * 4; i < tiles * kMergeTile; i += kSmallThreads * 4) {
+    u32x4 k;
+    if (i + 4 <= a.n) {
+      k = *reinterpret_cast<const u32x4*>(a.key_in + i);
+    } else {
+#pragma unroll
+      for (uint32_t e = 0; e < 4; ++e) k[e] = i + e < a.n ? a.key_in[i + e] : 0xFFFFFFFFu;
     }
+    *reinterpret_cast<u32x4*>(keys + i) = k;
+  }
+  __syncthreads();
+  const uint32_t p0 = blockIdx.x * 64, me = p0 + lane, own = p0 / kMergeTile;
+  const uint32_t key = keys[me];
+  uint32_t below = 0;
+#pragma unroll 4
+  for (uint32_t t = wave; t < tiles; t += WAVES) {
+    // an equal key of an earlier tile counts, of a later one it does not
+    const uint32_t limit = key + (t < own ? 1u : 0u);
+    const uint32_t* tile = keys + t * kMergeTile;
+    uint32_t c = 0;
+#pragma unroll
+    for (uint32_t step = kMergeTile / 2; step > 0; step /= 2) c += tile[c + step - 1] < limit ? step : 0u;
+    c += tile[c] < limit ? 1u : 0u;
+    below += t == own ? me % kMergeTile : c;
+  }
+  __syncthreads();  // the keys are done with
+  keys[tid] = below;
+  __syncthreads();
+  if (wave != 0 || me >= a.n) return;
+  uint32_t rank = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < WAVES; ++w) rank += keys[w * 64 + lane];
+  a.key_out[rank] = key;
+  a.pos_out[rank] = a.pos_in[me];
+}
+
+// the runs of a list of up to kCountSort places, in one workgroup
+__global__ __launch_bounds__(kSmallThreads) void run_small_kernel(RunKArgs r) {
+  constexpr uint32_t PER = kCountSort / kSmallThreads;
+  __shared__ uint32_t wsum[kSmallThreads / 64];
+  const uint32_t tid = threadIdx.x, s0 = tid * PER;
+  uint32_t c = 0, last = s0 > 0 && s0 < r.n ? r.key[s0 - 1] : r.rows;
+#pragma unroll
+  for (uint32_t e = 0; e < PER; ++e) {
+    if (s0 + e >= r.n) continue;
+    const uint32_t k = r.key[s0 + e];
+    c += k < r.rows && k != last ? 1u : 0u;
     last = k;
     r.unique[s0 + e] = -1;
   }
   uint32_t all;
   const uint32_t before = block_exclusive<kSmallThreads>(c, wsum, &all);
-  for (uint32_t e = 0; e < span; e += 4)  // chunks are multiples of 4 places
-    if (s0 + e < r.n && (s0 + e) % r.ch == 0)
-      r.chunk_runs[(s0 + e) / r.ch] = before + __popc(starts & ((1u << e) - 1u));
+  if (s0 < r.n && s0 % r.ch == 0) r.chunk_runs[s0 / r.ch] = before;  // chunks are multiples of PER places
   if (tid < r.tiles) r.tile_runs[tid] = 0;  // chunk_runs count from the start of the list
   if (tid == 0) *r.count = (int32_t)all;
 }
@@ -739,12 +779,12 @@ int64_t embed_grad_workspace_bytes(int64_t n, int64_t rows, int32_t dim) {
 }
 
 template <bool GRAD_F32>
-static hipError_t launch_segments(SegKArgs& a, int32_t dout_f32, bool zero_first, hipStream_t stream) {
+static hipError_t launch_segments(SegKArgs& a, int32_t dout_f32, hipStream_t stream) {
   const unsigned per = 256u >> a.group_shift;
   const unsigned cols = (unsigned)((a.dim + (8 << a.group_shift) - 1) / (8 << a.group_shift));
   a.blocks = (a.chunks + per - 1) / per;
   int64_t zeros = 0;  // workgroups that write zeros
-  if (a.mode == ENGRAM_GRAD_DENSE && !zero_first) {
+  if (a.mode == ENGRAM_GRAD_DENSE) {
     const int64_t row_bytes = (int64_t)a.dim * (GRAD_F32 ? 4 : 2);
     const bool whole = a.grad_vec != 0 && row_bytes % 16 == 0;
     a.grad_vec = whole ? a.grad_vec : 0;
@@ -779,10 +819,7 @@ hipError_t launch_embed_grad(const EmbedGradArgs& g, hipStream_t stream) {
   const int64_t n = g.T * g.cols;
   const bool sparse = g.mode == ENGRAM_GRAD_SPARSE;
   const int32_t grad_vec = ((uintptr_t)g.grad % 16 == 0 && g.grad_ld * grad_size % 16 == 0) ? 1 : 0;
-  const int64_t grad_bytes = g.rows * g.dim * (int64_t)grad_size;
-  const bool small = n <= kSmallSort;
-  const bool zero_first = g.mode == ENGRAM_GRAD_DENSE && n > 0 && small && g.grad_ld == g.dim &&
-                          (uintptr_t)g.grad % 16 == 0 && grad_bytes > kZeroFirst;
+  const bool small = n <= kMergeSort;
   char* w = static_cast<char*>(g.work);
   RunKArgs r = {};
   if (n == 0 && sparse) {
@@ -821,15 +858,23 @@ hipError_t launch_embed_grad(const EmbedGradArgs& g, hipStream_t stream) {
     s.key_in = s.pos_in = nullptr;
     s.key_out = reinterpret_cast<uint32_t*>(w + p.key[0]);
     s.pos_out = reinterpret_cast<uint32_t*>(w + p.pos[0]);
-    char* const zero = static_cast<char*>(g.grad);
-    const int64_t zero_bytes = zero_first ? grad_bytes : 0;
-    // no more workgroups than CUs; of a shorter list the counts take less time than their sum
-    if (n > 64 * 128 || n <= 1024) launch_sort_small<1>(s, zero, zero_bytes, stream);
-    else if (n > 64 * 64) launch_sort_small<2>(s, zero, zero_bytes, stream);
-    else launch_sort_small<4>(s, zero, zero_bytes, stream);
-    if (n > 0 && sparse) {
-      r.key = s.key_out;
-      hipLaunchKernelGGL(run_small_kernel, dim3(1), dim3(kSmallThreads), 0, stream, r);
+    if (n > kCountSort) {
+      const unsigned tiles = (p.n + kMergeTile - 1) / kMergeTile;
+      static std::atomic<uint64_t> lds_set{0};
+      const hipError_t e =
+          ensure_dynamic_lds(reinterpret_cast<const void*>(&sort_merge_kernel), kMergeSort * 4, lds_set);
+      if (e != hipSuccess) return e;
+      hipLaunchKernelGGL(sort_tile_kernel, dim3(tiles), dim3(kSmallThreads), 0, stream, s);
+      s.key_in = s.key_out;
+      s.pos_in = s.pos_out;
+      cur = 1;
+      s.key_out = reinterpret_cast<uint32_t*>(w + p.key[1]);
+      s.pos_out = reinterpret_cast<uint32_t*>(w + p.pos[1]);
+      hipLaunchKernelGGL(sort_merge_kernel, dim3((p.n + 63) / 64), dim3(kSmallThreads), tiles * kMergeTile * 4, stream, s);
+    } else if (n > 1024) {  // the counts take less time than their sum in a shorter list
+      launch_count_all<4>(s, stream);
+    } else {
+      launch_count_all<1>(s, stream);
     }
   } else {
     for (uint32_t pass = 0; pass < passes; ++pass) {
@@ -846,11 +891,13 @@ hipError_t launch_embed_grad(const EmbedGradArgs& g, hipStream_t stream) {
       if (pass == 0) hipLaunchKernelGGL((sort_scatter_kernel<true>), grid, block, 0, stream, s);
       else hipLaunchKernelGGL((sort_scatter_kernel<false>), grid, block, 0, stream, s);
     }
-    if (sparse) {
-      r.key = reinterpret_cast<const uint32_t*>(w + p.key[cur]);
-      hipLaunchKernelGGL(run_count_kernel, dim3(p.tiles), dim3(256), 0, stream, r);
-      hipLaunchKernelGGL(run_scan_kernel, dim3(1), dim3(256), 0, stream, r);
-    }
+  }
+  r.key = reinterpret_cast<const uint32_t*>(w + p.key[cur]);
+  if (sparse && n <= kCountSort) {
+    hipLaunchKernelGGL(run_small_kernel, dim3(1), dim3(kSmallThreads), 0, stream, r);
+  } else if (sparse) {
+    hipLaunchKernelGGL(run_count_kernel, dim3(p.tiles), dim3(256), 0, stream, r);
+    hipLaunchKernelGGL(run_scan_kernel, dim3(1), dim3(256), 0, stream, r);
   }
   SegKArgs a;
   a.key = reinterpret_cast<const uint32_t*>(w + p.key[cur]);
@@ -883,8 +930,8 @@ hipError_t launch_embed_grad(const EmbedGradArgs& g, hipStream_t stream) {
   a.grad_vec = grad_vec;
   a.div_cols = s.div_cols;
   a.group_shift = p.shift;
-  return g.grad_f32 ? launch_segments<true>(a, g.dout_f32, zero_first, stream)
-                    : launch_segments<false>(a, g.dout_f32, zero_first, stream);
+  return g.grad_f32 ? launch_segments<true>(a, g.dout_f32, stream)
+                    : launch_segments<false>(a, g.dout_f32, stream);
 }
 
 }  // namespace engram

@@ -222,7 +222,7 @@ def test_embed_grad_long_runs(eng, n, kind):
     assert torch.equal(unique[:count].long(), torch.nonzero(terms).flatten())
 
 
-@pytest.mark.parametrize("n", [1, 63, 1023, 1024, 1025, 4096, 4097, 8192, 8193, 16_383, 16_384, 16_385])
+@pytest.mark.parametrize("n", [1, 63, 1023, 1024, 1025, 4096, 4097, 8192, 8193, 16_383, 16_384, 16_385, 32_768, 32_769])
 @pytest.mark.parametrize("rows", [1 << 27, 1 << 28, 384_006_168, 2**31 - 1])
 def test_embed_grad_names_rows_of_large_tables(eng, n, rows):
     """Ids of 28 to 31 bits, short lists and long ones: every id once by name, its places added in
