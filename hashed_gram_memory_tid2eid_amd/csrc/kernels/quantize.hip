@@ -20,6 +20,12 @@
 // whole lines, a row's maximum is a reduction over 16 lanes, and a column's one over the
 // thread's own rows, 4 lanes and 4 waves.  Transposed codes of a thread are 8 rows = 8 bytes
 // of a column; they cross LDS (16 KB) and leave as 128-byte lines.
+//
+// Memory bounds it.  Codes are written past the caches (16,381 x 4,096 fp32 both ways 72 us
+// against 84): 407 MB, 5.9 TB/s; 16,381 x 6,144 bf16 both ways 80 us, 5 TB/s; 65,536 x 6,144
+// bf16 both ways 431 us (3.7 TB/s: every tile of the transposed codes is 128 lines that lie
+// 64 KB apart).  An order of the tiles that keeps those lines together (4 to 32 rows of tiles
+// at a time) measured the same.
 
 namespace engram {
 

@@ -610,14 +610,16 @@ int engram_fp8_quantize(const void* d_x, int32_t x_dtype, int64_t M, int64_t K, 
 
 /* C[m][n] = sum over k of a[m][k] b[n][k], for operands of engram_fp8_quantize: the value
  * of a code is its scale times its e4m3fn value.  Accumulated in fp32, rounded once to
- * c_dtype (BF16 or F32).
+ * c_dtype (BF16 or F32).  For F32 every product is exact and every sum fp32.  For BF16 the
+ * 8-bit matrix instruction first adds up to 8 neighbouring products with some 16 bits below
+ * their largest (1.4e-5 of the result in the 2-norm, below a bf16 step of 4e-3).
  *   d_a [M][a_ld] codes with scales d_sa [K/128][M]; d_b [N][b_ld] codes with scales d_sb
  *   [K/128][N] (b_block_rows 1) or [K/128][ceil(N/128)] (b_block_rows 128); both scales of
  *   scale_kind.  K a multiple of 128 (codes past the matrix are zero); a_ld, b_ld >= K,
  *   multiples of 16, rows 16-byte aligned; d_c [M][c_ld].
  *   Scales are multiplied before they meet a sum: their products must be finite.
  *   d_work: engram_fp8_matmul_workspace(M, N, K) bytes (0 unless K is split over
- *   workgroups, which few rows need), 16-byte aligned.
+ *   workgroups, which products of few tiles and of a partly filled last round need), 16-byte aligned.
  * Host errors: ENGRAM_E_ARG, ENGRAM_E_ALIGN, ENGRAM_E_SCRATCH, ENGRAM_E_UNSUPPORTED (256
  * rows of codes past 2^31 bytes). */
 int engram_fp8_matmul_workspace(int64_t M, int64_t N, int64_t K, int64_t* bytes);
