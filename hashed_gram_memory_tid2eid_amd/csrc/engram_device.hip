@@ -2,6 +2,7 @@
 // per-device status word and every kernel of the Engram hot path (gfx950).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "internal.h"
