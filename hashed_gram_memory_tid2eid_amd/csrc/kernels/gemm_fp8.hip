@@ -364,16 +364,19 @@ __global__ __launch_bounds__(256) void gemm_fp8_join_kernel(GemmFp8KArgs a, int3
 // ---- few rows of A ----------------------------------------------------------------
 //
 // Up to 16 MT rows (MT 1 or 2): the weight's bytes are the work, and what counts is how many of them are
-// on their way.  One workgroup owns 16 columns and all of K, its 8 waves every eighth k block
+// on their way.  One workgroup owns 16 columns and all of K, its 16 waves every 16th k block
 // of them, straight from memory into the operand registers (no LDS, no stages): 256
-// workgroups hold 4,096 columns, each wave some 8 KB in flight.  The waves' sums meet in LDS
-// and are added in wave order; there is no second launch and no workspace.
+// workgroups hold 4,096 columns, each wave some 6 KB of weight in flight.  The waves' sums meet
+// in LDS and are added in wave order; there is no second launch and no workspace.
+// Weights from memory, 4,096 columns, K 6,144: 16 rows 11.4 us, 32 rows 14.8; with 8 waves of 4
+// blocks in flight 13.3 and 17.7, of 6 blocks 11.6 and 14.7 (but K 19,584 28 against 25), with
+// 16 waves of 2 blocks 11.8 and 14.6.  Latency bounds it: 25 MB take 4 us of memory's rate.
 
-constexpr int kFewWaves = 8;
+constexpr int kFewWaves = 16;
 
 template <int MT, bool WIDE, bool E8M0, bool B_ROWS>
 __device__ __forceinline__ void gemm_fp8_few_rows(const GemmFp8KArgs& a) {
-  constexpr int U = 4;  // k blocks in flight
+  constexpr int U = 3;  // k blocks in flight
   __shared__ f32x4 part[kFewWaves][MT][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lrow = lane & 15, lk = lane >> 4;
@@ -491,9 +494,10 @@ struct GemmFp8Plan {
   int splits;
 };
 
-// Up to this many rows the few-row kernel runs.  4,096 columns, K 6,144: 16 rows 9 us or less
-// (the host's time per call) against 16 with 128 x 128 tiles and K split over 8 workgroups,
-// 32 rows 14 against 16; at 64 rows both take 17, and at 128 it took 28 against 19.
+// Up to this many rows the few-row kernel runs.  4,096 columns, K 6,144, weights in the last
+// cache: 16 rows 9 us or less (the host's time per call) against 16 with 128 x 128 tiles and K
+// split over 8 workgroups, 32 rows 14 against 16; at 64 rows both take 17, and at 128 it took
+// 28 against 19 (8 waves a workgroup).
 constexpr int64_t kFewRows = 32;
 
 // 256 x 256 tiles, one workgroup per CU, from 192 of them on; the tiles of a last, partly
