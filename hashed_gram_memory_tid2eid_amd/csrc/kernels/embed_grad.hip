@@ -31,6 +31,7 @@ constexpr int kCountSort = 4096;  // up to this many places are ranked by counti
 constexpr int kMergeTile = 256, kMergeSort = 32768;  // up to this many by tiles
 constexpr int kSegThreads = 256;
 constexpr int kUnit = 32;         // chunks per unit
+constexpr int64_t kChunkLanes = 131072;  // lanes that a longer chunk has to leave: 8 waves on every CU
 constexpr int kFewUnits = 16;     // up to this many units, runs add their heads without unit sums
                                   // (up to 32: 3,000 places 2 us less, all of one row 70 us more)
 constexpr uint32_t kZeroScan = 2048;  // places that are looked at one by one for rows without one
@@ -747,7 +748,7 @@ static EmbedGradPlan embed_grad_plan(int64_t n, int32_t dim) {
   // waves on every CU; more places make fewer partial rows.  At least the places in flight of
   // a lane (3,000 places of 128 added to their rows: 16.5 us, in chunks of 8 17.9)
   const int64_t lanes = n * (p.pdim / 8);
-  p.ch = lanes / 32 >= 131072 ? 32 : lanes / 16 >= 131072 ? 16 : lanes / 8 >= 131072 ? 8 : 4;
+  p.ch = lanes / 32 >= kChunkLanes ? 32 : lanes / 16 >= kChunkLanes ? 16 : lanes / 8 >= kChunkLanes ? 8 : 4;
   p.chunks = (uint32_t)((n + p.ch - 1) / p.ch);
   p.units = (p.chunks + kUnit - 1) / kUnit;
   p.blocks = (uint32_t)((n + kSortTile - 1) / kSortTile);
@@ -773,9 +774,18 @@ static EmbedGradPlan embed_grad_plan(int64_t n, int32_t dim) {
   return p;
 }
 
+// What a gradient of up to n places needs at most.  Each longer chunk halves the partial rows,
+// so the last list with the shorter chunk may need more than n places do (dim 256: 32,767
+// places 17.7 MB, 32,768 9.1 MB); between these steps the need only grows.
 int64_t embed_grad_workspace_bytes(int64_t n, int64_t rows, int32_t dim) {
   (void)rows;
-  return embed_grad_plan(n, dim).bytes;
+  const EmbedGradPlan all = embed_grad_plan(n, dim);
+  int64_t most = all.bytes;
+  for (int64_t ch = 8; ch <= 32; ch *= 2) {
+    const int64_t last = (ch * kChunkLanes - 1) / (all.pdim / 8);  // the last list whose chunks are shorter
+    if (last < n) most = std::max(most, embed_grad_plan(last, dim).bytes);
+  }
+  return most;
 }
 
 template <bool GRAD_F32>

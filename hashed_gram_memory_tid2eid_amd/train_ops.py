@@ -92,7 +92,7 @@ def engram_embed(table, ids, out, *, scale=1.0, seg_pitch=None, stream=None):
 
 
 def engram_embed_grad_workspace(places: int, rows: int, dim: int) -> int:
-    """Bytes of scratch a gradient of ``places`` = T * columns ids needs."""
+    """Bytes of scratch that gradients of up to ``places`` = T * columns ids need."""
     n = ctypes.c_int64(0)
     _check(_lib.engram_embed_grad_workspace(int(places), int(rows), int(dim), ctypes.byref(n)),
            "engram_embed_grad_workspace")

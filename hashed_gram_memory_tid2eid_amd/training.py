@@ -84,7 +84,8 @@ class SiteTraining:
         else:
             self.table_grads = [torch.zeros(t.shape, dtype=grad_dtype, device=dev) for t in tables]
             self.unique = self.count = [None] * len(tables)
-        # the split of a product changes with its shape: room for the largest it takes up to max_tokens
+        # the gradient's size serves every smaller call; the split of a product changes with its
+        # shape: room for the largest it takes up to max_tokens
         sizes = [engram_embed_grad_workspace(places, max(t.shape[0] for t in tables), info.row_dim)]
         sizes += [max(engram_fp8_matmul_workspace(n, h, K), engram_fp8_matmul_workspace(n, K, h),
                       engram_fp8_matmul_workspace(h, K, n)) for n in range(1, T + 1)]

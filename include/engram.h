@@ -577,7 +577,8 @@ typedef enum engram_grad_mode {
  *   d_dout [T][dout_ld] BF16 or F32; T * cols <= 2^30; d_grad by `mode`, BF16 or F32.
  *   SPARSE: d_unique int32 [T * cols] receives the distinct ids, then -1; d_count int32
  *   [1] their number.
- *   d_work: engram_embed_grad_workspace(T * cols, rows, dim) bytes, 256-byte aligned.
+ *   d_work: engram_embed_grad_workspace(T * cols, rows, dim) bytes, 256-byte aligned.  That
+ *   size never falls as places grow: a workspace for n places serves every call of up to n.
  * Host errors: ENGRAM_E_ARG, ENGRAM_E_ALIGN, ENGRAM_E_SCRATCH, ENGRAM_E_UNSUPPORTED.
  * Device error: ENGRAM_E_ROW_RANGE (such an id counts as -1: it has no gradient). */
 int engram_embed_grad_workspace(int64_t places, int64_t rows, int32_t dim, int64_t* bytes);
