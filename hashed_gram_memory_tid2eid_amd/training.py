@@ -16,7 +16,7 @@ from __future__ import annotations
 import torch
 
 from . import ENGRAM_TABLE_PER_SITE, Layout, engram_gate_add
-from .train_ops import (engram_embed, engram_embed_grad, engram_embed_grad_workspace, engram_fp8_matmul,
+from .train_ops import (_flat, engram_embed, engram_embed_grad, engram_embed_grad_workspace, engram_fp8_matmul,
                         engram_fp8_matmul_workspace, engram_fp8_quantize, engram_gate_add_backward)
 
 
@@ -75,7 +75,10 @@ class SiteTraining:
         self.dv_t, self.dv_ts = codes(h, tb), room(tb, h)
         self.d_rows = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
         self.d_weight = torch.empty((h, K), dtype=torch.float32, device=dev)
+        # what backward reads of a forward's arguments: copies, so that the caller may refill its own
         self.streams = torch.empty((T, hc_mult, h), dtype=torch.bfloat16, device=dev)  # as they were before the add
+        self.ids = torch.empty((T, 3 * info.heads), dtype=torch.int32, device=dev)
+        self.keep = torch.empty(T, dtype=torch.uint8, device=dev)
         places = T * self.table_cols
         if grad_mode == "sparse":
             self.table_grads = [torch.empty((places, info.row_dim), dtype=grad_dtype, device=dev) for _ in tables]
@@ -99,14 +102,13 @@ class SiteTraining:
             raise ValueError(f"weight must be {[self.hidden, self.k_pad]}")
         engram_fp8_quantize(weight, self.w_q, self.w_s, q_t=self.w_t, scales_t=self.w_ts, block_rows=128, stream=stream)
 
-    def _ids(self, row_ids, site, T):
-        info = self.layout.info
-        cols = row_ids.view(T, info.num_sites, 3 * info.heads)[:, site]
-        return [cols[:, n * self.table_cols:(n + 1) * self.table_cols] for n in range(len(self.tables))]
+    def _table_ids(self, n, T):
+        return self.ids[:T, n * self.table_cols:(n + 1) * self.table_cols]
 
     def forward(self, row_ids, streams, *, site: int = 0, keep=None, stream=None):
         """Adds the memory that row_ids (int32 [T][sites][3][H], engram_compress_hash) name into
-        ``streams`` (bf16 [T][hc][hidden], in place) and keeps what backward needs."""
+        ``streams`` (bf16 [T][hc][hidden], in place) and keeps what backward needs: a copy of the
+        site's ids, of keep (uint8 [T]) and of the streams, so that all three may be refilled."""
         T = streams.shape[0]
         if not 1 <= T <= self.max_tokens:
             raise ValueError(f"{T} tokens, construct with max_tokens for them (1 .. {self.max_tokens})")
@@ -114,11 +116,23 @@ class SiteTraining:
             raise ValueError(f"streams must be [T]{list(self.streams.shape[1:])}")
         if not 0 <= site < self.layout.info.num_sites:
             raise ValueError("site out of range")
+        info = self.layout.info
+        if not row_ids.is_cuda or row_ids.dtype != torch.int32:
+            raise TypeError("row_ids must be a device tensor of int32")
+        ids = row_ids.view(T, info.num_sites, 3 * info.heads)[:, site]
+        if keep is not None:
+            _flat(keep, "keep", torch.uint8)
+            if keep.numel() < T:
+                raise ValueError("keep too small")
         kb, tb = self.k_pad_blocks, -(-T // 128)
-        ids = self._ids(row_ids, site, T)
+        with _on(stream):
+            self.ids[:T].copy_(ids)
+            if keep is not None:
+                self.keep[:T].copy_(keep.view(-1)[:T])
+                keep = self.keep
         width = self.table_cols * self.seg
         for n, table in enumerate(self.tables):
-            engram_embed(table, ids[n], self.rows[:T, n * width:(n + 1) * width], scale=self.embed_scale,
+            engram_embed(table, self._table_ids(n, T), self.rows[:T, n * width:(n + 1) * width], scale=self.embed_scale,
                          seg_pitch=self.seg, stream=stream)
         engram_fp8_quantize(self.rows[:T], self.rows_q, self.rows_s[:kb * T].view(kb, T), q_t=self.rows_t,
                             scales_t=self.rows_ts[:tb * self.k_pad].view(tb, self.k_pad), stream=stream)
@@ -127,7 +141,7 @@ class SiteTraining:
         with _on(stream):
             self.streams[:T].copy_(streams)
         engram_gate_add(self.layout, self.v, streams, keep=keep, T=T, stream=stream)
-        self._pending = (T, ids, keep)
+        self._pending = (T, keep)
         return streams
 
     def backward(self, d_streams, *, stream=None):
@@ -136,7 +150,7 @@ class SiteTraining:
         when sparse).  One backward per forward."""
         if self._pending is None:
             raise RuntimeError("no forward is waiting for its backward")
-        T, ids, keep = self._pending
+        T, keep = self._pending
         if tuple(d_streams.shape) != (T,) + tuple(self.streams.shape[1:]):
             raise ValueError("d_streams must have the shape of the forward's streams")
         hb, tb = -(-self.hidden // 128), -(-T // 128)
@@ -149,7 +163,7 @@ class SiteTraining:
                           stream=stream)
         width = self.table_cols * self.seg
         for n, table in enumerate(self.tables):
-            engram_embed_grad(ids[n], self.d_rows[:T, n * width:(n + 1) * width], self.table_grads[n],
+            engram_embed_grad(self._table_ids(n, T), self.d_rows[:T, n * width:(n + 1) * width], self.table_grads[n],
                               rows=table.shape[0], scale=self.embed_scale, mode=self.grad_mode, seg_pitch=self.seg,
                               unique=self.unique[n], count=self.count[n], workspace=self.work, stream=stream)
         self._pending = None

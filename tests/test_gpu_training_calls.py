@@ -25,3 +25,36 @@ def test_every_call_up_to_max_tokens(eng, T):
     for a, b in zip(step(site, row_ids, x, dy, T), step(own, row_ids, x, dy, T)):
         assert torch.equal(a, b)
     assert eng.engram_get_error() == 0
+
+
+@pytest.mark.parametrize("sites, mode", [(1, "sparse"), (2, "accumulate")])
+def test_backward_after_the_callers_buffers_are_refilled(eng, sites, mode):
+    """row_ids, keep and streams of the forward hold the next call's values by the time of backward."""
+    L, tables, w, site, row_ids, x, dy, keep = make(eng, per_site=False, sites=sites, mode=mode)
+    other = eng.SiteTraining(L, tables, w, max_tokens=150, embed_scale=0.5, grad_mode=mode)
+    left = []
+    for s, refill in ((site, False), (other, True)):
+        ids, k, y, d = row_ids.clone(), keep.clone(), x.clone(), dy.clone()
+        s.forward(ids, y, site=sites - 1, keep=k)
+        if refill:
+            ids.copy_(ids.flip(0))
+            k.copy_(1 - k)
+            y.zero_()
+        s.backward(d)
+        torch.cuda.synchronize()
+        n = [int(c) if c is not None else t.shape[0] for c, t in zip(s.count, s.table_grads)]
+        left.append([d, s.d_weight, s.dv] + [g[:c] for g, c in zip(s.table_grads, n)])
+    for a, b in zip(*left):
+        assert torch.equal(a, b)
+
+
+def test_forward_refuses_ids_and_masks_it_would_convert(eng):
+    L, tables, w, site, row_ids, x, dy, keep = make(eng, per_site=True)
+    with pytest.raises(TypeError):
+        site.forward(row_ids.long(), x.clone())
+    with pytest.raises(TypeError):
+        site.forward(row_ids.cpu(), x.clone())
+    with pytest.raises(TypeError):
+        site.forward(row_ids, x.clone(), keep=keep.bool())
+    with pytest.raises(ValueError):
+        site.forward(row_ids, x.clone(), keep=keep[:20])
