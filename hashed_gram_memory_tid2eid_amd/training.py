@@ -108,7 +108,8 @@ class SiteTraining:
     def forward(self, row_ids, streams, *, site: int = 0, keep=None, stream=None):
         """Adds the memory that row_ids (int32 [T][sites][3][H], engram_compress_hash) name into
         ``streams`` (bf16 [T][hc][hidden], in place) and keeps what backward needs: a copy of the
-        site's ids, of keep (uint8 [T]) and of the streams, so that all three may be refilled."""
+        site's ids, of keep (uint8 [T]) and of the streams, so that all three may be refilled.
+        A forward that waits for its backward is dropped by the next."""
         T = streams.shape[0]
         if not 1 <= T <= self.max_tokens:
             raise ValueError(f"{T} tokens, construct with max_tokens for them (1 .. {self.max_tokens})")
@@ -125,6 +126,7 @@ class SiteTraining:
             if keep.numel() < T:
                 raise ValueError("keep too small")
         kb, tb = self.k_pad_blocks, -(-T // 128)
+        self._pending = None  # from here on the buffers of an earlier forward are written over
         with _on(stream):
             self.ids[:T].copy_(ids)
             if keep is not None:

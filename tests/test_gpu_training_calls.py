@@ -58,3 +58,26 @@ def test_forward_refuses_ids_and_masks_it_would_convert(eng):
         site.forward(row_ids, x.clone(), keep=keep.bool())
     with pytest.raises(ValueError):
         site.forward(row_ids, x.clone(), keep=keep[:20])
+
+
+def test_a_forward_that_fails_leaves_nothing_for_backward(eng):
+    """Streams of the wrong type are turned down by the gate, behind the projection: the buffers no
+    longer hold the forward before, and there is no backward of it."""
+    L, tables, w, site, row_ids, x, dy, keep = make(eng, per_site=True)
+    site.forward(row_ids, x.clone())
+    with pytest.raises(TypeError):
+        site.forward(row_ids.flip(0), x.float())
+    with pytest.raises(RuntimeError):
+        site.backward(dy.clone())
+    # arguments that are turned down before anything is written leave it waiting
+    y, want = dy.clone(), dy.clone()
+    site.forward(row_ids, x.clone())
+    with pytest.raises(ValueError):
+        site.forward(row_ids, x.clone(), site=1)
+    with pytest.raises(TypeError):
+        site.backward(dy.float())
+    site.backward(y)
+    other = eng.SiteTraining(L, tables, w, max_tokens=150, embed_scale=0.5)
+    other.forward(row_ids, x.clone())
+    other.backward(want)
+    assert torch.equal(y, want)
