@@ -157,6 +157,7 @@ class SiteTraining:
             raise ValueError("d_streams must have the shape of the forward's streams")
         hb, tb = -(-self.hidden // 128), -(-T // 128)
         engram_gate_add_backward(self.v, self.streams[:T], d_streams, d_streams, self.dv, keep=keep, stream=stream)
+        self._pending = None  # d_streams is replaced: what is left cannot be started again
         dvs, dvts = self.dv_s[:hb * T].view(hb, T), self.dv_ts[:tb * self.hidden].view(tb, self.hidden)
         engram_fp8_quantize(self.dv[:T], self.dv_q, dvs, q_t=self.dv_t, scales_t=dvts, stream=stream)
         engram_fp8_matmul(self.dv_q[:T], dvs, self.w_t, self.w_ts, self.d_rows[:T], workspace=self.work, stream=stream)
@@ -168,7 +169,6 @@ class SiteTraining:
             engram_embed_grad(self._table_ids(n, T), self.d_rows[:T, n * width:(n + 1) * width], self.table_grads[n],
                               rows=table.shape[0], scale=self.embed_scale, mode=self.grad_mode, seg_pitch=self.seg,
                               unique=self.unique[n], count=self.count[n], workspace=self.work, stream=stream)
-        self._pending = None
         return d_streams
 
     @property

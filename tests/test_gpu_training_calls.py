@@ -81,3 +81,16 @@ def test_a_forward_that_fails_leaves_nothing_for_backward(eng):
     other.forward(row_ids, x.clone())
     other.backward(want)
     assert torch.equal(y, want)
+
+
+def test_a_backward_that_fails_cannot_be_started_again(eng):
+    """What fails behind the gate's gradient has replaced d_streams: a second run would apply it twice."""
+    L, tables, w, site, row_ids, x, dy, keep = make(eng, per_site=True)
+    site.forward(row_ids, x.clone())
+    work, site.work = site.work, site.work[:0]
+    d = dy.clone()
+    with pytest.raises(eng.EngramError):
+        site.backward(d)
+    site.work = work
+    with pytest.raises(RuntimeError):
+        site.backward(d)
