@@ -97,9 +97,12 @@ class SiteTraining:
         self.load_weight(weight, stream=stream)
 
     def load_weight(self, weight, *, stream=None):
-        """Takes a [hidden][k_pad] weight over as 8-bit codes, in both the forms its products read."""
+        """Takes a [hidden][k_pad] weight over as 8-bit codes, in both the forms its products read.
+        A forward that waits for its backward is dropped: its gradients are those of the weight
+        that is written over."""
         if tuple(weight.shape) != (self.hidden, self.k_pad):
             raise ValueError(f"weight must be {[self.hidden, self.k_pad]}")
+        self._pending = None
         engram_fp8_quantize(weight, self.w_q, self.w_s, q_t=self.w_t, scales_t=self.w_ts, block_rows=128, stream=stream)
 
     def _table_ids(self, n, T):

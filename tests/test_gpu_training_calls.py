@@ -94,3 +94,12 @@ def test_a_backward_that_fails_cannot_be_started_again(eng):
     site.work = work
     with pytest.raises(RuntimeError):
         site.backward(d)
+
+
+def test_a_new_weight_drops_the_forward_of_the_old_one(eng):
+    """backward multiplies by the weight of its forward, which load_weight writes over."""
+    L, tables, w, site, row_ids, x, dy, keep = make(eng, per_site=True)
+    site.forward(row_ids, x.clone())
+    site.load_weight(w * 2)
+    with pytest.raises(RuntimeError):
+        site.backward(dy.clone())
