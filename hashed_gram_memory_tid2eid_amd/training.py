@@ -27,7 +27,8 @@ class SiteTraining:
     order, as the layout says.  weight: [hidden][k_pad] bf16 or fp32 (columns of segment
     padding zero).  scales: "f32" or "e8m0".  grad_mode: "sparse" (one row per distinct id;
     the tables may then be of any size) or "accumulate" (added into ``table_grads``, tensors
-    like the tables, which the caller clears)."""
+    like the tables, which the caller clears).  stream: takes the weight over, behind all that
+    the current stream holds."""
 
     def __init__(self, layout: Layout, tables, weight, *, max_tokens: int, embed_scale: float = 1.0,
                  scales: str = "f32", grad_mode: str = "sparse", grad_dtype=torch.float32, hc_mult: int = 4,
@@ -94,6 +95,12 @@ class SiteTraining:
                       engram_fp8_matmul_workspace(h, K, n)) for n in range(1, T + 1)]
         self.work = torch.empty(max(sizes), dtype=torch.uint8, device=dev)
         self._pending = None
+        if stream is not None:
+            # the buffers belong to the current stream: its zeros, and what it still does to memory
+            # that they take over, come before the first call on `stream`
+            here = torch.cuda.current_stream(dev)
+            with _on(stream):
+                torch.cuda.current_stream(dev).wait_stream(here)
         self.load_weight(weight, stream=stream)
 
     def load_weight(self, weight, *, stream=None):

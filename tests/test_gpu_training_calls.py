@@ -103,3 +103,24 @@ def test_a_new_weight_drops_the_forward_of_the_old_one(eng):
     site.load_weight(w * 2)
     with pytest.raises(RuntimeError):
         site.backward(dy.clone())
+
+
+def test_construction_for_another_stream(eng):
+    """The current stream is still busy when the site is made: the weight it writes and the zeros of
+    the gradients come before what the site does on its stream."""
+    L, tables, w, plain, row_ids, x, dy, keep = make(eng, per_site=False, mode="accumulate")
+    side, ready, late = torch.cuda.Stream(), w.clone(), torch.zeros_like(w)
+    got, want = (x.clone(), dy.clone()), (x.clone(), dy.clone())
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)  # some 20 ms
+    late.copy_(ready)
+    site = eng.SiteTraining(L, tables, late, max_tokens=150, embed_scale=0.5, grad_mode="accumulate", stream=side)
+    site.forward(row_ids, got[0], stream=side)
+    site.backward(got[1], stream=side)
+    torch.cuda.synchronize()
+    plain.forward(row_ids, want[0])
+    plain.backward(want[1])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(site.d_weight, plain.d_weight)
+    for a, b in zip(site.table_grads, plain.table_grads):
+        assert torch.equal(a, b)
