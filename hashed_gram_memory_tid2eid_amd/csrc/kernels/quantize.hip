@@ -13,7 +13,10 @@
 // The quotient without a division per element: r = fl(1 / s) once per block, y = fl(x r),
 // and one correction y + (x - y s) r with the residual exact in an fma.  With r correctly
 // rounded this is the correctly rounded quotient (Markstein, "Computation of elementary
-// functions on the IBM RISC System/6000 processor", 1990).
+// functions on the IBM RISC System/6000 processor", 1990).  The residual has to stay clear of
+// the end of fp32: a wave that meets a scale under 2^-64 does its codes once more, with x and s
+// both 2^64 times as large (left as they are, 4 to 6% of the quotients that lie on a tie gave
+// the other code for s around 2^-122).
 //
 // A workgroup of 4 waves holds a tile of 16 RT rows x 128 columns in registers: lane l of
 // wave w holds 8 consecutive columns (l % 16) of RT consecutive rows, so a wave's loads are
@@ -31,6 +34,7 @@ namespace engram {
 
 constexpr int kQuantThreads = 256;
 constexpr float kE4m3Max = 448.0f;
+constexpr float kQuantUp = 0x1p64f;  // what x and s of a small block are multiplied by
 
 struct QuantScale {
   float s, r;       // the scale and its reciprocal
@@ -57,8 +61,16 @@ __device__ __forceinline__ QuantScale quant_scale(uint32_t amax_bits) {
   return o;
 }
 
-template <bool E8M0>
+// whether a float scale is too small for quotients as they are: under 2^-64, but not 2^-126, which
+// divides exactly (and is the scale of every empty block)
+__device__ __forceinline__ bool quant_small(const QuantScale& q) { return q.held - 0x00800001u < 0x1F800000u - 0x00800001u; }
+
+template <bool E8M0, bool SMALL>
 __device__ __forceinline__ float quant_quotient(float x, const QuantScale& q) {
+  if (SMALL && quant_small(q)) {
+    const float v = x * kQuantUp, s = q.s * kQuantUp, r = q.r * (1.0f / kQuantUp), y = v * r;
+    return fmaf(fmaf(-y, s, v), r, y);
+  }
   const float y = x * q.r;
   if (E8M0) return y;  // a power of two: exact
   return fmaf(fmaf(-y, q.s, x), q.r, y);
@@ -86,9 +98,10 @@ struct QuantKArgs {
 __device__ __forceinline__ int quant_slot(int col, int g) { return col * 16 + (g ^ ((col >> 3) & 15)); }
 
 // (tiles of 128 rows: three waves a SIMD; left alone the compiler takes registers for two, and
-// 16,381 x 6,144 bf16 both ways took 103 us instead of 80; four spill)
+// 16,381 x 6,144 bf16 both ways took 103 us instead of 80; four spill.  The transpose alone
+// fits five)
 template <bool X_F32, bool E8M0, bool ROWS, bool COLS, bool BLOCK, int RT>
-__global__ __launch_bounds__(kQuantThreads, RT == 8 ? 3 : 1) void fp8_quantize_kernel(QuantKArgs a) {
+__global__ __launch_bounds__(kQuantThreads, RT < 8 ? 1 : ROWS || BLOCK ? 3 : 5) void fp8_quantize_kernel(QuantKArgs a) {
   static_assert(!(COLS || BLOCK) || RT == 8, "column blocks need a tile of 128 rows");
   constexpr int TILE_M = 16 * RT;
   __shared__ uint64_t tile[COLS ? 128 * 16 : 1];
@@ -143,6 +156,14 @@ __global__ __launch_bounds__(kQuantThreads, RT == 8 ? 3 : 1) void fp8_quantize_k
   QuantScale one = {};
   if (BLOCK) {
     one = quant_scale<E8M0>(block_max);
+    if (!E8M0 && quant_small(one)) {  // uniform
+      one.s *= kQuantUp;
+      one.r *= 1.0f / kQuantUp;
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i][j] *= kQuantUp;
+    }
     if (tid == 0) {
       if (ROWS) {
         const int64_t at = (int64_t)kb * a.MB + mt;
@@ -157,10 +178,13 @@ __global__ __launch_bounds__(kQuantThreads, RT == 8 ? 3 : 1) void fp8_quantize_k
     }
   }
 
-  if (ROWS) {
+  // the codes along the rows; returns whether a scale of the thread's is small
+  auto row_codes = [&](auto careful) -> bool {
+    bool small = false;
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int64_t m = m0 + r0 + i;
+      if (careful()) __builtin_amdgcn_sched_barrier(0);  // one row after the other, in few registers
       QuantScale q = one;
       if (!BLOCK) {
         uint32_t rm = 0;
@@ -169,6 +193,7 @@ __global__ __launch_bounds__(kQuantThreads, RT == 8 ? 3 : 1) void fp8_quantize_k
 #pragma unroll
         for (int off = 8; off >= 1; off >>= 1) rm = max(rm, (uint32_t)__shfl_xor((int)rm, off, 64));
         q = quant_scale<E8M0>(rm);
+        small |= quant_small(q);
       }
       if (m >= a.M) continue;
       if (!BLOCK && c == 0) {
@@ -178,22 +203,31 @@ __global__ __launch_bounds__(kQuantThreads, RT == 8 ? 3 : 1) void fp8_quantize_k
       }
       float y[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = quant_quotient<E8M0>(x[i][j], q);
+      for (int j = 0; j < 8; ++j) y[j] = quant_quotient<E8M0, careful()>(x[i][j], q);
       uint2 o;
       o.x = pack_e4m3x4(y[0], y[1], y[2], y[3]);
       o.y = pack_e4m3x4(y[4], y[5], y[6], y[7]);
       __builtin_nontemporal_store((uint64_t)o.x | ((uint64_t)o.y << 32), reinterpret_cast<uint64_t*>(a.q + m * a.q_ld + k0));
     }
+    return small;
+  };
+  if constexpr (ROWS) {
+    const bool small = row_codes(std::false_type());
+    if (!E8M0 && !BLOCK && __any(small)) row_codes(std::true_type());
   }
 
-  if constexpr (COLS) {
+  // the codes along the columns, into LDS
+  auto column_codes = [&](auto careful) -> bool {
+    bool small = false;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int col = c * 8 + j;
+      if (careful()) __builtin_amdgcn_sched_barrier(0);
       QuantScale q = one;
       if (!BLOCK) {
         const uint32_t m4 = max(max(colmax[0][col], colmax[1][col]), max(colmax[2][col], colmax[3][col]));
         q = quant_scale<E8M0>(m4);
+        small |= quant_small(q);
         if (wave == 0 && lane < 16 && k0 + j < a.K) {
           const int64_t at = (int64_t)mt * a.K + k0 + j;
           if (E8M0) static_cast<uint8_t*>(a.st)[at] = (uint8_t)q.held;
@@ -202,10 +236,15 @@ __global__ __launch_bounds__(kQuantThreads, RT == 8 ? 3 : 1) void fp8_quantize_k
       }
       float y[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = quant_quotient<E8M0>(x[i % RT][j], q);
+      for (int i = 0; i < 8; ++i) y[i] = quant_quotient<E8M0, careful()>(x[i % RT][j], q);
       const uint64_t lo = pack_e4m3x4(y[0], y[1], y[2], y[3]), hi = pack_e4m3x4(y[4], y[5], y[6], y[7]);
       tile[quant_slot(col, r0 >> 3)] = lo | (hi << 32);
     }
+    return small;
+  };
+  if constexpr (COLS) {
+    const bool small = column_codes(std::false_type());
+    if (!E8M0 && !BLOCK && __any(small)) column_codes(std::true_type());
     __syncthreads();
     // 8 lanes write one column's 128 codes: thread -> column tid / 8 + 32 p, 16 bytes tid % 8
 #pragma unroll
