@@ -17,6 +17,8 @@ inline bool elt_aligned(const void* p, int32_t t) { return aligned(p, t == ENGRA
 constexpr int64_t kMax32 = 0x7FFFFFFF;
 // places of one lookup gradient: their sorted positions and byte sizes stay in 32 bits
 constexpr int64_t kMaxPlaces = (int64_t)1 << 30;
+// columns of a lookup gradient: rounded up to whole groups of lanes (2,048 columns) they stay there, too
+constexpr int32_t kMaxGradDim = 0x7FFFFFFF - 2047;
 
 int lookup_shape(int64_t rows, int32_t dim, int64_t T, int32_t cols, int64_t ids_ld, int64_t seg_pitch, int64_t ld) {
   if (rows < 1 || rows > kMax32 || dim < 1 || T < 0 || cols < 1) return ENGRAM_E_ARG;
@@ -58,7 +60,7 @@ extern "C" int engram_embed(const void* d_table, int32_t table_dtype, int64_t ro
 
 extern "C" int engram_embed_grad_workspace(int64_t places, int64_t rows, int32_t dim, int64_t* bytes) {
   if (!bytes || places < 0 || rows < 1 || rows > kMax32 || dim < 1) return ENGRAM_E_ARG;
-  if (places > kMaxPlaces) return ENGRAM_E_UNSUPPORTED;
+  if (places > kMaxPlaces || dim > kMaxGradDim) return ENGRAM_E_UNSUPPORTED;
   *bytes = engram::embed_grad_workspace_bytes(places, rows, dim);
   return ENGRAM_OK;
 }
@@ -73,7 +75,7 @@ extern "C" int engram_embed_grad(const int32_t* d_ids, int64_t T, int32_t cols, 
   const int rc = lookup_shape(rows, dim, T, cols, ids_ld, seg_pitch, dout_ld);
   if (rc != ENGRAM_OK) return rc;
   if (grad_ld < dim) return ENGRAM_E_ARG;
-  if (T > kMaxPlaces / cols) return ENGRAM_E_UNSUPPORTED;
+  if (T > kMaxPlaces / cols || dim > kMaxGradDim) return ENGRAM_E_UNSUPPORTED;
   const int64_t n = T * cols;
   const bool sparse = mode == ENGRAM_GRAD_SPARSE;
   if (sparse && !d_count) return ENGRAM_E_ARG;

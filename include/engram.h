@@ -574,7 +574,8 @@ typedef enum engram_grad_mode {
 /* The lookup's gradient: G[r][d] = scale * sum of dout[t][c * seg_pitch + d] over the
  * places (t, c) with ids[t * ids_ld + c] = r, summed in fp32 in an order fixed by the
  * ids, rounded once to grad_dtype.
- *   d_dout [T][dout_ld] BF16 or F32; T * cols <= 2^30; d_grad by `mode`, BF16 or F32.
+ *   d_dout [T][dout_ld] BF16 or F32; T * cols <= 2^30; dim <= 2^31 - 2,048; d_grad by `mode`,
+ *   BF16 or F32.
  *   SPARSE: d_unique int32 [T * cols] receives the distinct ids, then -1; d_count int32
  *   [1] their number.
  *   d_work: engram_embed_grad_workspace(T * cols, rows, dim) bytes, 256-byte aligned.  That

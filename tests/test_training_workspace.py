@@ -26,3 +26,17 @@ def test_gradient_workspace_serves_fewer_places(dim):
 def test_every_smaller_call_fits(cols, dim, max_tokens):
     most = eng.engram_embed_grad_workspace(max_tokens * cols, 1000, dim)
     assert all(eng.engram_embed_grad_workspace(T * cols, 1000, dim) <= most for T in range(1, max_tokens))
+
+
+def test_gradient_of_columns_past_32_bits_is_refused():
+    """Columns rounded up to whole groups of lanes have to fit 32 bits: the kernels count them so."""
+    widest = 2 ** 31 - 2048
+    assert eng.engram_embed_grad_workspace(1, 1, widest) > 0
+    work, P = 1 << 40, 1 << 20  # an aligned address that nothing reads
+    for dim in (widest + 1, 2 ** 31 - 1):
+        with pytest.raises(eng.EngramError):
+            eng.engram_embed_grad_workspace(1, 1, dim)
+        for mode in (0, 1, 2):
+            assert eng._lib.engram_embed_grad(P, 1, 1, 1, 1, dim, 1.0, P, eng.ENGRAM_DTYPE_BF16, dim, dim, mode, P,
+                                              eng.ENGRAM_DTYPE_F32, dim, P, P, P, work, None) == \
+                eng.STATUS["ENGRAM_E_UNSUPPORTED"]
