@@ -40,3 +40,12 @@ def test_gradient_of_columns_past_32_bits_is_refused():
             assert eng._lib.engram_embed_grad(P, 1, 1, 1, 1, dim, 1.0, P, eng.ENGRAM_DTYPE_BF16, dim, dim, mode, P,
                                               eng.ENGRAM_DTYPE_F32, dim, P, P, P, work, None) == \
                 eng.STATUS["ENGRAM_E_UNSUPPORTED"]
+
+
+@pytest.mark.parametrize("dim, lanes", [(122, 16), (256, 32), (4093, 512), (4096, 512)])
+def test_chunks_grow_where_enough_lanes_are_left(dim, lanes):
+    """A longer chunk halves the partial rows, so the workspace stays where it was for a while."""
+    for chunk in (8, 16, 32):
+        n = chunk * 131072 // lanes
+        before, last, first, behind = (eng.engram_embed_grad_workspace(m, 1000, dim) for m in (n - 64, n - 1, n, n + n // 4))
+        assert before < last == first == behind
