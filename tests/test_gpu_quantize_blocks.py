@@ -1,9 +1,9 @@
-"""The quantiser's blocks where a code is decided by the quotient's last bit.
+"""The quantiser's blocks where a code is decided by the quotient's last bit, and rows alone in many tiles.
 Codes and scales follow from single correctly rounded operations: compared bit for bit."""
 import pytest
 import torch
 
-from test_gpu_train_ops import DEV, F32, eng, gen, held, quantize_ref  # noqa: F401  (eng is a fixture)
+from test_gpu_train_ops import BF16, DEV, F32, eng, gen, held, quantize_ref, rough, up  # noqa: F401  (eng is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,21 @@ def test_small_blocks_beside_large_and_empty_ones(eng):
     for codes, scales, values in ((q, s, x), (qt, st, x.t())):
         wq, ws = quantize_ref(values, False)
         assert torch.equal(scales.cpu(), ws) and torch.equal(codes.cpu().float(), wq.float())
+
+
+@pytest.mark.parametrize("M, K", [(1344, 6130), (1345, 6130), (1400, 6130), (8192, 1024), (8193, 1024), (16_381, 700),
+                                  (65_537, 130), (4000, 2049)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("e8m0", [False, True])
+def test_rows_alone(eng, M, K, dtype, e8m0):
+    """Tiles of 16 rows up to 2,048 tiles of 32 x 128, of 64 rows from there on: on both sides, with rows and
+    columns past the last whole tile."""
+    assert (-(-K // 128) * -(-M // 32) > 2048) == ((M, K) not in ((1344, 6130), (8192, 1024)))
+    x = rough(gen(M + K), M, K, dtype)
+    wq, ws = quantize_ref(x, e8m0)
+    q = torch.full((M + 1, up(K) + 16), 9, dtype=torch.uint8, device=DEV)
+    s = torch.empty(ws.shape, dtype=torch.uint8 if e8m0 else F32, device=DEV)
+    eng.engram_fp8_quantize(x, q[:M], s)
+    assert torch.equal(s.cpu(), held(ws, e8m0))
+    assert torch.equal(q[:M, :up(K)].cpu().view(torch.float8_e4m3fn).float(), wq.float())
+    assert bool((q[:M, up(K):] == 9).all()) and bool((q[M] == 9).all())
