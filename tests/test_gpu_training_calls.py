@@ -124,3 +124,39 @@ def test_construction_for_another_stream(eng):
     assert torch.equal(site.d_weight, plain.d_weight)
     for a, b in zip(site.table_grads, plain.table_grads):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("sites", [1, 2])
+def test_a_captured_step_replays_with_new_inputs(eng, sites):
+    """Forward and backward in one graph; every replay, after the inputs were refilled, against the same
+    calls made eagerly."""
+    L, tables, w, site, row_ids, x, dy, keep = make(eng, per_site=False, sites=sites, mode="accumulate")
+    other = eng.SiteTraining(L, tables, w, max_tokens=150, embed_scale=0.5, grad_mode="accumulate")
+    ids, k, y, d = row_ids.clone(), keep.clone(), x.clone(), dy.clone()
+
+    def run(s):
+        s.forward(ids, y, site=sites - 1, keep=k)
+        s.backward(d)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(site)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(site)
+    for turn in range(4):
+        left = []
+        for s, go in ((site, graph.replay), (other, lambda: run(other))):
+            ids.copy_(row_ids.roll(7 * turn, 0))
+            k.copy_(keep.roll(turn, 0))
+            y.copy_(x.roll(turn, 0))
+            d.copy_(dy.roll(3 * turn, 0))
+            for t in s.table_grads:
+                t.zero_()
+            go()
+            torch.cuda.synchronize()
+            left.append([t.clone() for t in (y, d, s.d_weight, *s.table_grads)])
+        for a, b in zip(*left):
+            assert torch.equal(a, b), turn
