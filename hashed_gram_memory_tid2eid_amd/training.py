@@ -7,7 +7,14 @@ gradient), projects them with the 8-bit weight and adds the gated result into th
 residual streams.  ``SiteTraining.backward`` takes the gradient of the streams after the
 add and leaves the gradient of the streams before it in its place, the weight's gradient
 in ``d_weight`` and the tables' in ``table_grads``.  The tables and the float weight are the
-caller's; an optimizer steps them and ``load_weight`` takes the new weight over.
+caller's; an optimizer steps them and ``load_weight`` takes the new weight over.  ``d_weight`` is
+the gradient of the last backward alone, in both modes of the tables' gradients: a caller who
+adds up several calls adds it to a sum of its own.
+
+What lies between the operators is kept in few bits where it meets fewer right after.  The
+rows are bf16 (of fp32 tables, too): they are only read as e4m3 codes, whose step is 16 times
+a bf16 one.  The gradient of the rows is bf16, half its bytes to write and read; it comes from
+8-bit operands, each off by up to 2^-4, and the lookup's gradient adds it in fp32.
 
 Every call only enqueues kernels on one stream; nothing is allocated after construction.
 """

@@ -604,7 +604,7 @@ typedef enum engram_fp8_scale {
  * Either pair may be NULL, not both; both come from one pass over x.  q_ld (qt_ld) is at
  * least K (M) rounded up to 128 and a multiple of 16, d_q and d_qt 16-byte aligned; codes
  * from K (M) up to that multiple of 128 are written as zero.  A block that holds an
- * infinity or a NaN becomes all NaN.
+ * infinity or a NaN becomes all NaN, zeros past the matrix that belong to it included.
  * Host errors: ENGRAM_E_ARG, ENGRAM_E_ALIGN, ENGRAM_E_UNSUPPORTED. */
 int engram_fp8_quantize(const void* d_x, int32_t x_dtype, int64_t M, int64_t K, int64_t x_ld, int32_t scale_kind,
                         int32_t block_rows, uint8_t* d_q, int64_t q_ld, void* d_scales, uint8_t* d_qt, int64_t qt_ld,
@@ -612,14 +612,18 @@ int engram_fp8_quantize(const void* d_x, int32_t x_dtype, int64_t M, int64_t K, 
 
 /* C[m][n] = sum over k of a[m][k] b[n][k], for operands of engram_fp8_quantize: the value
  * of a code is its scale times its e4m3fn value.  Accumulated in fp32, rounded once to
- * c_dtype (BF16 or F32).  For F32 every product is exact and every sum fp32.  For BF16 the
+ * c_dtype (BF16 or F32).  For F32 every product is exact (e8m0 scales from 2^-124 on: below,
+ * scale times code leaves bf16's range at its small end) and every sum fp32.  For BF16 the
  * 8-bit matrix instruction first adds up to 8 neighbouring products with some 16 bits below
- * their largest (1.4e-5 of the result in the 2-norm, below a bf16 step of 4e-3).
+ * their largest: 1.4e-5 of the result in the 2-norm, where rounding to bf16 takes 1.7e-3; of
+ * results whose terms cancel to under a hundredth of a typical one it takes 2.6e-3.  A caller
+ * who needs fp32 sums there takes an F32 result.
  *   d_a [M][a_ld] codes with scales d_sa [K/128][M]; d_b [N][b_ld] codes with scales d_sb
  *   [K/128][N] (b_block_rows 1) or [K/128][ceil(N/128)] (b_block_rows 128); both scales of
  *   scale_kind.  K a multiple of 128 (codes past the matrix are zero); a_ld, b_ld >= K,
  *   multiples of 16, rows 16-byte aligned; d_c [M][c_ld].
- *   Scales are multiplied before they meet a sum: their products must be finite.
+ *   Float scales are multiplied before they meet a sum: their products must be finite, and
+ *   below 2^-126 they lose bits.
  *   d_work: engram_fp8_matmul_workspace(M, N, K) bytes (0 unless K is split over
  *   workgroups, which products of few tiles and of a partly filled last round need), 16-byte aligned.
  * Host errors: ENGRAM_E_ARG, ENGRAM_E_ALIGN, ENGRAM_E_SCRATCH, ENGRAM_E_UNSUPPORTED (256
