@@ -15,8 +15,9 @@
 // write past the caches, which then keep table rows instead.  65,536 x 24 rows of 256 bf16
 // (Zipf ids, 4M rows, 805 MB written and some 140 MB of distinct rows): 157 us where the rows
 // are in the last cache (with ordinary stores 272), 246 us where they come from memory; fp32
-// output 264 (464) and 421.  Uniform ids read as much as they write, 1.6 GB in 266 us, 6.1 TB/s:
-// it is memory's rate for single rows between the writes that bounds it.  In the order 8, 2, 1
+// output 264 (464) and 421.  Uniform ids read as much as they write, 1.6 GB in 266 us, 6.1 TB/s;
+// that the Zipf ids' 940 MB take 246 is neither their bytes nor their number of requests, and
+// is not explained.  In the order 8, 2, 1
 // chunks in flight 259, 257, 304 us from memory; rows read past the caches 282.
 
 namespace engram {

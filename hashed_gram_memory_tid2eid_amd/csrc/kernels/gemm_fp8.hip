@@ -29,10 +29,11 @@
 // threads as rows of A and B) loads entry t.
 //
 // What bounds it is the issue of a SIMD, which the matrix and the vector instructions share:
-// about 4.7 cycles times their number.  65,536 x 4,096 over 6,144 (3.3e12 operations), per scale
-// type: bf16 C e8m0 1,305 us (2.53 PFLOP/s), fp32 1,500 us; fp32 C e8m0 2,290 us (1.44), fp32
-// 2,580 us (1.28): the widening is a vector instruction per 4 codes, an fp32 scale an fma per
-// result and block more.
+// about 4.7 cycles times their number.  65,536 x 4,096 over 6,144 (3.3e12 operations), medians of 40
+// calls, least 2 to 4% lower: bf16 C with e8m0 scales 1,303 us (2.53 PFLOP/s), fp32 1,487 us (2.22),
+// fp32 with one per row of B 1,697 us (1.94); fp32 C 2,268 us (1.45), 2,431 us (1.36) and 2,863 us
+// (1.15): the widening is a vector instruction per 4 codes, an fp32 scale an fma per result and
+// block more.
 // Measured and not taken: 32 x 32 matrix shapes (the same; e8m0 15% slower), 4 waves of 128 x 128
 // (the accumulators leave the vector registers, and the folds pay the moves), B widened during
 // the last row tile before the barrier (spills), a branch between full and edge tiles around the
@@ -369,9 +370,10 @@ __global__ __launch_bounds__(256) void gemm_fp8_join_kernel(GemmFp8KArgs a, int3
 // of them, straight from memory into the operand registers (no LDS, no stages): 256
 // workgroups hold 4,096 columns, each wave some 6 KB of weight in flight.  The waves' sums meet
 // in LDS and are added in wave order; there is no second launch and no workspace.
-// Weights from memory, 4,096 columns, K 6,144: 16 rows 11.4 us, 32 rows 14.8; with 8 waves of 4
-// blocks in flight 13.3 and 17.7, of 6 blocks 11.6 and 14.7 (but K 19,584 28 against 25), with
-// 16 waves of 2 blocks 11.8 and 14.6.  Latency bounds it: 25 MB take 4 us of memory's rate.
+// Weights from memory, 4,096 columns, K 6,144, in a replayed graph: 1 row 7.3 us, 16 rows 9.1, 32
+// rows 12.2 (cached 6.3, 8.0, 11.0).  Called one by one from the host 16 and 32 rows took 11.4 and
+// 14.8; with 8 waves of 4 blocks in flight 13.3 and 17.7, of 6 blocks 11.6 and 14.7 (but K 19,584 28
+// against 25), with 16 waves of 2 blocks 11.8 and 14.6.  25 MB take 4 us of memory's rate.
 
 constexpr int kFewWaves = 16;
 
@@ -495,10 +497,10 @@ struct GemmFp8Plan {
   int splits;
 };
 
-// Up to this many rows the few-row kernel runs.  4,096 columns, K 6,144, weights in the last
-// cache: 16 rows 9 us or less (the host's time per call) against 16 with 128 x 128 tiles and K
-// split over 8 workgroups, 32 rows 14 against 16; at 64 rows both take 17, and at 128 it took
-// 28 against 19 (8 waves a workgroup).
+// Up to this many rows the few-row kernel runs, which holds two row tiles.  4,096 columns, K 6,144,
+// in a replayed graph, against 128 x 128 tiles with K split over 8 workgroups: weights from memory,
+// 1 row 7.3 us against 17.2, 16 rows 9.1 against 18.7, 32 rows 12.2 against 19.6; cached 6.3 against
+// 14.3, 8.0 against 16.3, 11.0 against 17.1.
 constexpr int64_t kFewRows = 32;
 
 // 256 x 256 tiles, one workgroup per CU, from 192 of them on; the tiles of a last, partly

@@ -25,9 +25,10 @@
 // of a column; they cross LDS (16 KB) and leave as 128-byte lines.
 //
 // Memory bounds it.  Codes are written past the caches (16,381 x 4,096 fp32 both ways 72 us
-// against 84): 407 MB, 5.9 TB/s; 16,381 x 6,144 bf16 both ways 80 us, 5 TB/s; 65,536 x 6,144
-// bf16 both ways 431 us (3.7 TB/s: every tile of the transposed codes is 128 lines that lie
-// 64 KB apart).  An order of the tiles that keeps those lines together (4 to 32 rows of tiles
+// against 84): 407 MB in 74 us, 5.5 TB/s; 16,381 x 6,144 bf16 both ways 88 us, 4.7 TB/s; 65,536 x
+// 6,144 bf16 rows alone 210 us (5.8 TB/s), both ways 423 us (3.9 TB/s: every tile of the
+// transposed codes is 128 lines that lie 64 KB apart); 4,096 x 6,144 fp32 in blocks of 128 x 128,
+// both codes, 23 us (6.6 TB/s, x in the last cache).  An order of the tiles that keeps those lines together (4 to 32 rows of tiles
 // at a time) measured the same.
 
 namespace engram {
@@ -98,7 +99,7 @@ struct QuantKArgs {
 __device__ __forceinline__ int quant_slot(int col, int g) { return col * 16 + (g ^ ((col >> 3) & 15)); }
 
 // (tiles of 128 rows: three waves a SIMD; left alone the compiler takes registers for two, and
-// 16,381 x 6,144 bf16 both ways took 103 us instead of 80; four spill.  The transpose alone
+// 16,381 x 6,144 bf16 both ways took 103 us where three took 80; four spill.  The transpose alone
 // fits five)
 template <bool X_F32, bool E8M0, bool ROWS, bool COLS, bool BLOCK, int RT>
 __global__ __launch_bounds__(kQuantThreads, RT < 8 ? 1 : ROWS || BLOCK ? 3 : 5) void fp8_quantize_kernel(QuantKArgs a) {
