@@ -144,6 +144,12 @@ _sig("engram_fp8_quantize", [_P, _i32, _i64, _i64, _i64, _i32, _i32, _P, _i64, _
 _sig("engram_fp8_matmul_workspace", [_i64, _i64, _i64, ctypes.POINTER(_i64)])
 _sig("engram_fp8_matmul", [_P, _i64, _P, _P, _i64, _P, _i32, _i32, _i64, _i64, _i64, _P, _i32, _i64, _P, _i64, _P])
 _sig("engram_gate_add_backward", [_P, _P, _P, _P, _i32, _i32, _P, _P, _i32, _P])
+_sig("engram_block_plan", [_P, _P, _i32, _i32, _P, _i64, _i32, _P, _P, _i32, _P, _P, _P, _i32, _P, _P, _P])
+_sig("engram_block_release", [_P, _i64, _i32, _P, _P, _i32, _i32, _P, _i32, _P])
+_sig("engram_beam_select_workspace", [_i32, _i32, _i32, _i32, ctypes.POINTER(_i64)])
+_sig("engram_beam_select", [_P, _i32, _i64, _i32, _i32, _i32, _P, _P, _i32, _i32, _P, _P, _P, _P, _P, _i64, _P])
+_sig("engram_beam_reorder", [_P, _i32, _i32, _P, _P, _P, _P, _P, _P, _P, _i64, _i32, _P, _i32, _P, _i32, _P, _P, _P])
+_sig("engram_state_copy", [_P, _i64, _i64, _i64, _i64, _i64, _P, _P, _i32, _P])
 _sig("engram_strerror", [ctypes.c_int], ctypes.c_char_p)
 _sig("engram_host_device_pointer", [_P, ctypes.POINTER(_P)])
 _sig("engram_get_error", [_P])
@@ -731,5 +737,8 @@ from .train_ops import (  # noqa: E402  (needs the functions above)
     ENGRAM_FP8_SCALE_E8M0, ENGRAM_FP8_SCALE_F32, ENGRAM_GRAD_ACCUMULATE, ENGRAM_GRAD_DENSE, ENGRAM_GRAD_SPARSE,
     engram_embed, engram_embed_grad, engram_embed_grad_workspace, engram_fp8_matmul, engram_fp8_matmul_workspace,
     engram_fp8_quantize, engram_gate_add_backward)
+from .serve_ops import (  # noqa: E402  (needs the functions above)
+    engram_beam_reorder, engram_beam_select, engram_beam_select_workspace, engram_block_plan, engram_block_release,
+    engram_state_copy)
 from .runtime import Engram, pad_weight  # noqa: E402  (needs the functions above)
 from .training import SiteTraining  # noqa: E402

@@ -59,7 +59,7 @@ static int current_device(int32_t* dev) {
 
 // The store belongs to the device that is current now, and was made for a layout
 // with the same compressed vocabulary and pad token.
-static int store_usable(const engram_store* st, const engram_layout* L) {
+int engram::store_usable(const engram_store* st, const engram_layout* L) {
   if (!st) return ENGRAM_E_ARG;
   if (L && (st->vc != L->desc.compressed_vocab || st->pad_token_id != L->desc.pad_token_id))
     return ENGRAM_E_ARG;
@@ -71,7 +71,7 @@ static int store_usable(const engram_store* st, const engram_layout* L) {
 
 static int store_op(const engram_store* st, const int32_t* d_slots, int32_t n, int32_t* d_ids,
                     int op, hipStream_t stream) {
-  int rc = store_usable(st, nullptr);
+  int rc = engram::store_usable(st, nullptr);
   if (rc != ENGRAM_OK) return rc;
   if (d_slots && n < 0) return ENGRAM_E_ARG;
   const int32_t count = d_slots ? n : st->num_slots;
@@ -155,7 +155,7 @@ extern "C" int engram_store_rollback(const engram_layout* L, const int32_t* d_ti
   if (!L || S < 0 || T < 0) return ENGRAM_E_ARG;
   if (S == 0) return ENGRAM_OK;
   if (!d_tid2eid || !d_slots || !d_cu_seqlens || !d_keep_len) return ENGRAM_E_ARG;
-  const int rc = store_usable(st, L);
+  const int rc = engram::store_usable(st, L);
   if (rc != ENGRAM_OK) return rc;
   if (T > 0 && !d_eids) return ENGRAM_E_ARG;
   if (d_seq_start && !d_snapshot) return ENGRAM_E_ARG;  // continuing sequences need their tails
@@ -188,7 +188,7 @@ extern "C" int engram_compress_hash(const engram_layout* L, const int32_t* d_tid
   if (T > 0 && (S < 1 || !d_tokens || !d_eids || !d_row_ids)) return ENGRAM_E_ARG;
   if (S > 0 && !d_cu_seqlens) return ENGRAM_E_ARG;
   if (store) {
-    const int rc = store_usable(store, L);
+    const int rc = engram::store_usable(store, L);
     if (rc != ENGRAM_OK) return rc;
   }
   int32_t* d_store = store ? store->ids : nullptr;
@@ -341,7 +341,7 @@ extern "C" int engram_lookup_decode(const engram_layout* L, const int32_t* d_tid
   if (T < 0 || !d_tid2eid || !d_tables || !d_scales) return ENGRAM_E_ARG;
   if (d_slots && !store) return ENGRAM_E_NEED_STORE;
   if (store) {
-    const int rc = store_usable(store, L);
+    const int rc = engram::store_usable(store, L);
     if (rc != ENGRAM_OK) return rc;
   }
   if (T == 0) return ENGRAM_OK;

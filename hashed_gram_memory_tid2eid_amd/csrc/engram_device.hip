@@ -60,3 +60,6 @@ hipError_t read_and_clear_device_error(hipStream_t stream, int* status) {
 #include "kernels/quantize.hip"
 #include "kernels/gemm_fp8.hip"
 #include "kernels/gate_backward.hip"
+#include "kernels/blocks.hip"
+#include "kernels/beam_select.hip"
+#include "kernels/beam_reorder.hip"

@@ -305,6 +305,94 @@ struct GateBackwardArgs {
 };
 hipError_t launch_gate_backward(const GateBackwardArgs& a, hipStream_t stream);
 
+// ---- serving operators (serve.cpp) -------------------------------------------
+
+constexpr int kPlanMaxRows = 8192;  // their sums stay in one workgroup's LDS
+
+struct PlanArgs {
+  const int32_t* past;   // [R]
+  const int32_t* fresh;  // [R] new tokens
+  int32_t R, page_size;
+  int32_t* tables;       // [R][table_ld]
+  int64_t table_ld;
+  int32_t max_blocks;
+  const uint32_t* free;  // bitmap of num_pages
+  uint32_t* free_out;
+  int32_t num_pages;
+  int32_t* cu_seqlens;   // [R + 1]
+  uint8_t* seq_start;    // [R] or null
+  int32_t* lens;         // [R] or null; may be past
+  int32_t T;
+  int32_t* positions;    // [T] or null
+  int64_t* token_slots;  // [T] or null
+  int32_t granule_words; // set by the launcher: words of the bitmap counted together
+  int32_t tokens_here;   // set by the launcher: tokens are done by the planning workgroup
+};
+hipError_t launch_block_plan(const PlanArgs& a, hipStream_t stream);
+
+struct ReleaseArgs {
+  const int32_t* tables;
+  int64_t table_ld;
+  int32_t max_blocks;
+  const int32_t* lens;   // [R]
+  const uint8_t* flags;  // [R]
+  int32_t R, page_size;
+  uint32_t* free;
+  int32_t num_pages;
+};
+hipError_t launch_block_release(const ReleaseArgs& a, hipStream_t stream);
+
+struct SelectArgs {
+  const void* logits;    // [G * K][ld] bf16 or f32
+  int32_t f32;
+  int64_t ld;
+  int32_t G, K, V;
+  const float* scores;   // [G][K]
+  const uint8_t* done;   // [G][K] or null
+  int32_t end_token, n;
+  int32_t* tokens;       // [G][n]
+  int32_t* parents;      // [G][n]
+  float* out_scores;     // [G][n]
+  uint8_t* out_done;     // [G][n] or null
+  float2* parts;         // workspace: maximum and sum of every piece, set by the launcher
+  unsigned long long* keys;  // workspace: the n largest of every piece, set by the launcher
+  int32_t splits;        // pieces of a row, set by the launcher
+  void* work;
+};
+int64_t beam_select_workspace_bytes(int32_t G, int32_t K, int32_t V, int32_t n);
+hipError_t launch_beam_select(const SelectArgs& a, hipStream_t stream);
+
+struct ReorderArgs {
+  const int32_t* parents;  // [G][K]
+  int32_t G, K;
+  int32_t* store;          // [num_slots][3] or null
+  int32_t num_slots;
+  const int32_t* slots;    // [G][K] or null
+  int32_t* slots_out;
+  int32_t* slot_src;       // pairs, or null
+  int32_t* slot_dst;
+  const int32_t* tables;   // [G * K][table_ld] or null
+  int32_t* tables_out;
+  int64_t table_ld;
+  int32_t max_blocks;
+  const int32_t* lens;     // [G * K]
+  int32_t page_size;
+  uint32_t* free;          // or null
+  int32_t num_pages;
+  int32_t* page_src;       // pairs, or null
+  int32_t* page_dst;
+};
+hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t stream);
+
+struct StateCopyArgs {
+  char* state;
+  int64_t planes, plane_pitch, rows, row_pitch, row_bytes;
+  const int32_t* src;      // [n]
+  const int32_t* dst;      // [n]
+  int32_t n;
+};
+hipError_t launch_state_copy(const StateCopyArgs& a, hipStream_t stream);
+
 // The wkv handle's dispatch (abi.cpp), shared by the entry points that bring their
 // own scratch: the argument check of a T-token call, its plan, the planned
 // projection into d_v or the split-K slices at d_partials, and the gated add from
@@ -317,5 +405,7 @@ int wkv_gate_from(const engram_layout* L, const engram_wkv* W, float* d_v, const
                   int32_t hc_mult, const uint8_t* d_keep, void* d_streams, int32_t T,
                   hipStream_t stream);
 int hip_error_status(hipError_t e);
+// A store for calls on the device that is current now (abi.cpp); L null: of any layout.
+int store_usable(const engram_store* st, const engram_layout* L);
 
 }  // namespace engram

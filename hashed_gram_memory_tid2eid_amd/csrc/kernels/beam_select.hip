@@ -1,0 +1,464 @@
+// beam_select.hip -- beam search's selection over beams and vocabulary.  Included into
+// engram_device.hip.
+//
+//   total(b, v) = score_b + x_bv - log sum_u exp(x_bu),  the n largest of a request's K * V
+//
+// Two launches.  The first cuts every row of logits into pieces of 256 lanes x NV loads of 16
+// bytes, one workgroup each, and reads each logit once: a piece stays in registers while its
+// maximum m is found, then its sum of exp(x - m) and its n largest logits.  Those need no sort
+// of the piece: lane i of the four waves stands for the maximum of its elements, and a bound
+// that n of these 64 maxima reach is reached by n elements at least and by few more, so the
+// elements that reach it go to a list in LDS, and each finds its rank by counting the larger
+// ones.  Keys of (logit, lowest token first) are all different, so ranks are, too, whatever
+// the order in which the list was filled.  A list that overflows (many equal logits) is not
+// used; the piece's n largest are then taken one by one.
+// The second launch, one workgroup a request, adds the pieces' sums in 64 bits, turns the keys
+// into totals and selects among them by the same bound, list and count.
+
+namespace engram {
+
+constexpr int kSelectThreads = 256;
+constexpr int kSelectList = 1024;
+constexpr int kMergeList = 2048;
+constexpr float kLowest = -3.402823466e38f;
+constexpr float kLog2e = 1.44269504088896341f;
+
+// Unsigned numbers in the order of the floats (no NaN).
+__device__ __forceinline__ uint32_t in_order(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_order(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
+}
+__device__ __forceinline__ uint32_t high_in_order(double x) {
+  const uint32_t h = (uint32_t)__double2hiint(x);
+  return (h & 0x80000000u) ? ~h : h | 0x80000000u;
+}
+
+// Larger logits first, then lower tokens.  (x + 0 makes -0 and 0 one value.)
+__device__ __forceinline__ unsigned long long select_key(float x, int token) {
+  return (unsigned long long)in_order(x + 0.0f) << 32 | (uint32_t)~token;
+}
+__device__ __forceinline__ float key_logit(unsigned long long key) { return from_order((uint32_t)(key >> 32)); }
+__device__ __forceinline__ int key_token(unsigned long long key) { return (int)~(uint32_t)key; }
+
+// The largest bound of `bits` leading bits that at least n lanes' values reach (n <= 64; 0 if
+// fewer than n lanes have any).
+__device__ __forceinline__ uint32_t bound_of_lanes(uint32_t value, int n, int bits) {
+  uint32_t bound = 0;
+  for (int b = 31; b >= 32 - bits; --b) {
+    const uint32_t next = bound | 1u << b;
+    if (__popcll(__ballot(value >= next)) >= n) bound = next;
+  }
+  return bound;
+}
+
+// kVec logits from element e of a row on; those from V on are -inf.  A lane's elements go by
+// their place in the row, not by the row's place in its 16-byte lines (a load may start at any
+// element), so that equal rows have equal sums, and beams with equal totals keep their order.
+template <typename T>
+struct Logits;
+template <>
+struct Logits<float> {
+  static constexpr int kVec = 4;
+  typedef float raw_t __attribute__((ext_vector_type(4)));
+  typedef raw_t anywhere_t __attribute__((aligned(4)));
+  raw_t raw;
+  __device__ __forceinline__ void load(const float* x, int e, int V) {
+    if (e + kVec <= V) {
+      raw = *reinterpret_cast<const anywhere_t*>(x + e);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) raw[i] = e + i < V ? x[e + i] : -INFINITY;
+  }
+  __device__ __forceinline__ float at(int i) const { return raw[i]; }
+};
+template <>
+struct Logits<uint16_t> {  // bf16
+  static constexpr int kVec = 8;
+  typedef uint32_t raw_t __attribute__((ext_vector_type(4)));
+  typedef raw_t anywhere_t __attribute__((aligned(2)));
+  raw_t raw;
+  __device__ __forceinline__ void load(const uint16_t* x, int e, int V) {
+    if (e + kVec <= V) {
+      raw = *reinterpret_cast<const anywhere_t*>(x + e);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; i += 2) {
+      const uint32_t lo = e + i < V ? x[e + i] : 0xFF80u;
+      const uint32_t hi = e + i + 1 < V ? x[e + i + 1] : 0xFF80u;
+      raw[i / 2] = hi << 16 | lo;
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float(i & 1 ? raw[i / 2] & 0xFFFF0000u : raw[i / 2] << 16);
+  }
+};
+
+// Beams whose logits are not read: done, or without a finite score.
+__device__ __forceinline__ bool beam_is_live(const SelectArgs& a, int row) {
+  return (a.done == nullptr || a.done[row] == 0) && isfinite(a.scores[row]);
+}
+
+template <typename T, int NV>
+__global__ __launch_bounds__(kSelectThreads) void beam_select_rows_kernel(SelectArgs a) {
+  constexpr int kVec = Logits<T>::kVec;
+  const int row = (int)(blockIdx.x / (unsigned)a.splits), piece = (int)(blockIdx.x % (unsigned)a.splits);
+  if (!beam_is_live(a, row)) return;
+  __shared__ float lane_max[4][64];
+  __shared__ float wave_sum[4];
+  __shared__ unsigned long long list[kSelectList];
+  __shared__ int listed;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const T* x = static_cast<const T*>(a.logits) + row * a.ld;
+  const int e0 = (piece * NV * kSelectThreads + tid) * kVec;
+  Logits<T> v[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) v[j].load(x, e0 + j * kSelectThreads * kVec, a.V);
+  if (tid == 0) listed = 0;
+
+  float most[NV];  // of each load: most of them reach no bound and are passed over whole
+  float mine = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    most[j] = v[j].at(0);
+#pragma unroll
+    for (int i = 1; i < kVec; ++i) most[j] = fmaxf(most[j], v[j].at(i));
+    mine = fmaxf(mine, most[j]);
+  }
+  lane_max[wave][lane] = mine;
+  __syncthreads();
+  const float of_lane = fmaxf(fmaxf(lane_max[0][lane], lane_max[1][lane]), fmaxf(lane_max[2][lane], lane_max[3][lane]));
+  float m = of_lane;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  // the bound keeps 16 bits: exact for bf16, and 2^-8 below the n-th of the maxima for fp32
+  const uint32_t reach = bound_of_lanes(in_order(of_lane), a.n, 16);
+  const float bound = reach <= in_order(kLowest) ? kLowest : from_order(reach);
+
+  // exp(x - m) as a power of two; an infinity or a NaN among the logits makes the sum a NaN
+  const float base = m == -INFINITY ? 0.0f : m;
+  float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) sum[i & 1] += __builtin_amdgcn_exp2f((v[j].at(i) - base) * kLog2e);
+    if (most[j] >= bound) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        if (v[j].at(i) >= bound) {
+          const int place = atomicAdd(&listed, 1);
+          if (place < kSelectList) list[place] = select_key(v[j].at(i), e0 + j * kSelectThreads * kVec + i);
+        }
+      }
+    }
+  }
+  float s = sum[0] + sum[1];
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off, 64);
+  if (lane == 0) wave_sum[wave] = s;
+  __syncthreads();
+  if (tid == 0) {
+    a.parts[blockIdx.x] = make_float2(m, (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]));
+  }
+  unsigned long long* out = a.keys + (int64_t)blockIdx.x * a.n;
+  const int count = listed;
+  if (count <= kSelectList) {
+    for (int i = tid; i < count; i += kSelectThreads) {
+      const unsigned long long key = list[i];
+      int rank = 0;
+      for (int k = 0; k < count; ++k) rank += list[k] > key ? 1 : 0;
+      if (rank < a.n) out[rank] = key;
+    }
+    for (int i = count + tid; i < a.n; i += kSelectThreads) out[i] = 0;
+    return;
+  }
+  // too many equal ones: one by one, each the largest key below the last
+  __shared__ unsigned long long wave_best[4];
+  unsigned long long last = ~0ull;
+  for (int r = 0; r < a.n; ++r) {
+    unsigned long long best = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const float f = v[j].at(i);
+        const unsigned long long key = select_key(f, e0 + j * kSelectThreads * kVec + i);
+        if (f >= kLowest && key < last && key > best) best = key;
+      }
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+      const unsigned long long other = __shfl_xor(best, off, 64);
+      best = other > best ? other : best;
+    }
+    __syncthreads();  // the last round's are read
+    if (lane == 0) wave_best[wave] = best;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) best = wave_best[w] > best ? wave_best[w] : best;
+    if (tid == 0) out[r] = best;
+    last = best;
+  }
+}
+
+// What a request's beams add to their logits: total = (score + (x - most)) - norm.
+struct MergeBeams {
+  double score[64], most[64], norm[64];
+  int kind[64];  // 0: no candidates, 1: live, 2: done
+};
+
+__device__ __forceinline__ double beam_total(const MergeBeams& s, int b, unsigned long long key) {
+  return (s.score[b] + ((double)key_logit(key) - s.most[b])) - s.norm[b];
+}
+
+__device__ __forceinline__ bool goes_before(double ta, int ba, unsigned long long ka, double tb, int bb,
+                                            unsigned long long kb) {
+  return ta > tb || (ta == tb && (ba < bb || (ba == bb && ka > kb)));
+}
+
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a) {
+  __shared__ MergeBeams beams;
+  __shared__ uint32_t lane_max[THREADS];
+  __shared__ double totals[kMergeList];
+  __shared__ unsigned long long keys[kMergeList];
+  __shared__ uint8_t of_beam[kMergeList];
+  __shared__ int listed;
+  const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int S = a.splits, K = a.K, n = a.n;
+  if (tid == 0) listed = 0;
+  for (int b = wave; b < K; b += THREADS / 64) {
+    const int row = g * K + b;
+    const float score = a.scores[row];
+    int kind = !isfinite(score) ? 0 : a.done != nullptr && a.done[row] != 0 ? 2 : 1;
+    double most = 0.0, norm = 0.0;
+    if (kind == 1) {
+      const float2* part = a.parts + (int64_t)row * S;
+      float m = -INFINITY;
+      for (int i = lane; i < S; i += 64) m = fmaxf(m, part[i].x);
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+      if (isfinite(m)) {
+        double z = 0.0;
+        for (int i = lane; i < S; i += 64) z += (double)part[i].y * exp((double)part[i].x - (double)m);
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) z += __shfl_xor(z, off, 64);
+        most = (double)m;
+        norm = log(z);
+        if (!(z == z)) kind = 0;
+      } else {
+        kind = 0;
+      }
+    }
+    if (lane == 0) {
+      beams.score[b] = (double)score;
+      beams.most[b] = most;
+      beams.norm[b] = norm;
+      beams.kind[b] = kind;
+    }
+  }
+  __syncthreads();
+
+  // a bound that n of 64 lanes reach with the first, largest, key of their pieces
+  const int pieces = K * S;
+  const unsigned long long* all = a.keys + (int64_t)g * pieces * n;
+  uint32_t mine = 0;
+  for (int l = tid; l < pieces; l += THREADS) {
+    const int b = l / S;
+    if (beams.kind[b] != 1) continue;
+    const unsigned long long key = all[(int64_t)l * n];
+    if (key != 0) mine = max(mine, high_in_order(beam_total(beams, b, key)));
+  }
+  lane_max[tid] = mine;
+  __syncthreads();
+  uint32_t of_lane = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w) of_lane = max(of_lane, lane_max[w * 64 + lane]);
+  const uint32_t bound = bound_of_lanes(of_lane, n, 32);
+
+  auto push = [&](double total, int b, unsigned long long key) {
+    const int place = atomicAdd(&listed, 1);
+    if (place < kMergeList) {
+      totals[place] = total;
+      keys[place] = key;
+      of_beam[place] = (uint8_t)b;
+    }
+  };
+  const bool many = (int64_t)pieces * n > 8 * THREADS;  // then a piece's first key says whether to look at the others
+  for (int64_t i = tid; i < (int64_t)pieces * n; i += THREADS) {
+    const int l = (int)(i / n), b = l / S;
+    if (beams.kind[b] != 1) continue;
+    if (many) {
+      const unsigned long long head = all[(int64_t)l * n];
+      if (head == 0 || high_in_order(beam_total(beams, b, head)) < bound) continue;
+    }
+    const unsigned long long key = all[i];
+    if (key == 0) continue;
+    const double total = beam_total(beams, b, key);
+    if (high_in_order(total) >= bound) push(total, b, key);
+  }
+  if (tid < K && beams.kind[tid] == 2) push(beams.score[tid], tid, select_key(0.0f, a.end_token));
+  __syncthreads();
+
+  auto write = [&](int r, double total, int b, unsigned long long key) {
+    const int64_t at = (int64_t)g * n + r;
+    const int token = key_token(key);
+    a.tokens[at] = token;
+    a.parents[at] = b;
+    a.out_scores[at] = (float)total;
+    if (a.out_done != nullptr) a.out_done[at] = beams.kind[b] == 2 || token == a.end_token ? 1 : 0;
+  };
+  auto write_none = [&](int r) {
+    const int64_t at = (int64_t)g * n + r;
+    a.tokens[at] = -1;
+    a.parents[at] = -1;
+    a.out_scores[at] = -INFINITY;
+    if (a.out_done != nullptr) a.out_done[at] = 0;
+  };
+  const int count = listed;
+  if (count <= kMergeList) {
+    for (int i = tid; i < count; i += THREADS) {
+      const double total = totals[i];
+      const unsigned long long key = keys[i];
+      const int b = of_beam[i];
+      int rank = 0;
+      for (int k = 0; k < count; ++k) rank += goes_before(totals[k], of_beam[k], keys[k], total, b, key) ? 1 : 0;
+      if (rank < n) write(rank, total, b, key);
+    }
+    for (int r = count + tid; r < n; r += THREADS) write_none(r);
+    return;
+  }
+  // too many equal ones: one by one, each the first behind the last
+  __shared__ int wave_b[THREADS / 64];
+  double last_t = INFINITY;
+  unsigned long long last_k = 0;
+  int last_b = -1;
+  for (int r = 0; r < n; ++r) {
+    double best_t = -INFINITY;
+    unsigned long long best_k = 0;
+    int best_b = -1;
+    auto consider = [&](double t, int b, unsigned long long key) {
+      if (goes_before(last_t, last_b, last_k, t, b, key) &&
+          (best_b < 0 || goes_before(t, b, key, best_t, best_b, best_k))) {
+        best_t = t;
+        best_k = key;
+        best_b = b;
+      }
+    };
+    for (int64_t i = tid; i < (int64_t)pieces * n; i += THREADS) {
+      const int b = (int)(i / n) / S;
+      if (beams.kind[b] != 1) continue;
+      const unsigned long long key = all[i];
+      if (key != 0) consider(beam_total(beams, b, key), b, key);
+    }
+    if (tid < K && beams.kind[tid] == 2) consider(beams.score[tid], tid, select_key(0.0f, a.end_token));
+    auto join = [&](double t, int b, unsigned long long key) {
+      if (b >= 0 && (best_b < 0 || goes_before(t, b, key, best_t, best_b, best_k))) {
+        best_t = t;
+        best_k = key;
+        best_b = b;
+      }
+    };
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+      const double t = __shfl_xor(best_t, off, 64);
+      const unsigned long long key = __shfl_xor(best_k, off, 64);
+      const int b = __shfl_xor(best_b, off, 64);
+      join(t, b, key);
+    }
+    __syncthreads();  // the last round's are read
+    if (lane == 0) {
+      totals[wave] = best_t;
+      keys[wave] = best_k;
+      wave_b[wave] = best_b;
+    }
+    __syncthreads();
+    for (int w = 0; w < THREADS / 64; ++w) join(totals[w], wave_b[w], keys[w]);
+    if (tid == 0) {
+      if (best_b >= 0)
+        write(r, best_t, best_b, best_k);
+      else
+        write_none(r);
+    }
+    if (best_b < 0) {  // nothing is left (best_* are the same in every thread)
+      for (int q = r + 1 + tid; q < n; q += THREADS) write_none(q);
+      return;
+    }
+    last_t = best_t;
+    last_k = best_k;
+    last_b = best_b;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Pieces of a row of V elements.
+static int select_splits(int V, int vec, int nv) {
+  const int per = nv * vec * kSelectThreads;
+  return (V + per - 1) / per;
+}
+
+// Loads a lane: as many as leave this many workgroups, up to 8.
+constexpr int kSelectGroups = 1024;
+
+static int select_loads(int64_t rows, int V, int vec) {
+  int nv = 8;
+  while (nv > 1 && rows * select_splits(V, vec, nv) < kSelectGroups) nv >>= 1;
+  return nv;
+}
+
+// Pieces that calls of up to G requests can have, in either type.
+static int64_t select_pieces(int64_t rows, int V) {
+  int64_t most = 0;
+  for (int vec = 4; vec <= 8; vec += 4)
+    for (int nv = 1; nv <= 8; nv <<= 1) {
+      // rows for which nv is taken: fewer than twice the loads would need
+      int64_t r = rows;
+      if (nv < 8) r = std::min(r, (int64_t)(kSelectGroups - 1) / select_splits(V, vec, 2 * nv));
+      most = std::max(most, r * select_splits(V, vec, nv));
+    }
+  return most;
+}
+
+int64_t beam_select_workspace_bytes(int32_t G, int32_t K, int32_t V, int32_t n) {
+  return select_pieces((int64_t)G * K, V) * (int64_t)(sizeof(float2) + n * sizeof(unsigned long long));
+}
+
+template <typename T>
+static void launch_select_rows(const SelectArgs& a, int nv, hipStream_t stream) {
+  const dim3 grid((unsigned)((int64_t)a.G * a.K * a.splits)), block(kSelectThreads);
+  switch (nv) {
+    case 1: hipLaunchKernelGGL((beam_select_rows_kernel<T, 1>), grid, block, 0, stream, a); break;
+    case 2: hipLaunchKernelGGL((beam_select_rows_kernel<T, 2>), grid, block, 0, stream, a); break;
+    case 4: hipLaunchKernelGGL((beam_select_rows_kernel<T, 4>), grid, block, 0, stream, a); break;
+    default: hipLaunchKernelGGL((beam_select_rows_kernel<T, 8>), grid, block, 0, stream, a); break;
+  }
+}
+
+hipError_t launch_beam_select(const SelectArgs& args, hipStream_t stream) {
+  (void)hipGetLastError();  // drop a stale error another library left on this thread
+  SelectArgs a = args;
+  if (a.G == 0) return hipSuccess;
+  const int vec = a.f32 ? 4 : 8;
+  const int nv = select_loads((int64_t)a.G * a.K, a.V, vec);
+  a.splits = select_splits(a.V, vec, nv);
+  const int64_t pieces = (int64_t)a.G * a.K * a.splits;
+  a.keys = static_cast<unsigned long long*>(a.work);
+  a.parts = reinterpret_cast<float2*>(a.keys + pieces * a.n);
+  if (a.f32)
+    launch_select_rows<float>(a, nv, stream);
+  else
+    launch_select_rows<uint16_t>(a, nv, stream);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if ((int64_t)a.K * a.splits * a.n > 4096)
+    hipLaunchKernelGGL(beam_select_merge_kernel<1024>, dim3(a.G), dim3(1024), 0, stream, a);
+  else
+    hipLaunchKernelGGL(beam_select_merge_kernel<256>, dim3(a.G), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace engram

@@ -242,6 +242,9 @@ extern "C" const char* engram_strerror(int s) {
     case ENGRAM_E_UNSUPPORTED: return "unsupported shape";
     case ENGRAM_E_ID_RANGE: return "compressed id written to the store outside [0, compressed_vocab)";
     case ENGRAM_E_SCRATCH: return "call needs more scratch than the no-allocation entry point holds";
+    case ENGRAM_E_PAGES: return "fewer free pages than the call's new blocks";
+    case ENGRAM_E_PAGE_RANGE: return "block table names a page outside its pool";
+    case ENGRAM_E_PARENT_RANGE: return "beam's parent outside [-1, beams)";
     default: return "unknown status";
   }
 }

@@ -78,6 +78,9 @@ extern "C" {
 #define ENGRAM_E_UNSUPPORTED (-13) /* a valid but unimplemented shape (e.g. hc_mult != 4)   */
 #define ENGRAM_E_ID_RANGE (-14)    /* device: a compressed id written to the store is outside [0, V_c) */
 #define ENGRAM_E_SCRATCH (-15)     /* the call needs more scratch than engram_gated_residual_noalloc holds */
+#define ENGRAM_E_PAGES (-16)       /* device: fewer free pages than the call's new blocks    */
+#define ENGRAM_E_PAGE_RANGE (-17)  /* device: a block table names a page outside its pool    */
+#define ENGRAM_E_PARENT_RANGE (-18) /* device: a beam's parent outside [-1, beams)           */
 
 /* ---- element types ------------------------------------------------------ */
 typedef enum engram_dtype {
@@ -643,6 +646,129 @@ int engram_fp8_matmul(const uint8_t* d_a, int64_t a_ld, const void* d_sa, const 
  * bit for bit and gives dv = 0.  Errors as engram_gate_add. */
 int engram_gate_add_backward(const float* d_v, const void* d_streams, const uint8_t* d_keep, const void* d_dy,
                              int32_t hidden, int32_t hc_mult, void* d_dx, float* d_dv, int32_t T, hipStream_t stream);
+
+/* ---- serving operators --------------------------------------------------------- */
+/* What a serving loop needs around the rolling store ([vLLM-V41] forward: the hash takes
+ * query_start_loc, positions, slot_mapping and block_table of the batch; [VeOmni#1370]
+ * generate commit: sampler -> n-gram memory -> backbone in every step): the batch's index
+ * arrays and block tables, beam search's selection, and the states that follow it.  All are
+ * hot calls: nothing is allocated, nothing synchronises, every launch goes to `stream` and
+ * may be captured.  The same call gives the same bits.  Pointers are aligned to their
+ * element unless said otherwise.
+ *
+ * A pool of pages is a bitmap: bit i of word w of d_free [ceil(num_pages / 32)] is set while
+ * page 32 w + i is free (bits from num_pages on are ignored).  A block table's row r holds
+ * the page of block b (its tokens b * page_size .. ) in column b.  num_pages < 2^30,
+ * page_size * max_blocks < 2^31. */
+
+/* Block tables and slot maps of a batch, from request lengths on the device.  Row r has
+ * d_past[r] >= 0 tokens in its pages and brings d_new[r] >= 0:
+ *   d_cu_seqlens[r] = sum of d_new[0 .. r-1], d_cu_seqlens[R] their total;
+ *   d_lens[r] = d_past[r] + d_new[r];  d_seq_start[r] = d_past[r] == 0;
+ *   blocks ceil(past / page_size) .. ceil(lens / page_size) - 1 of row r get pages: the pool's
+ *   lowest free ones, to rows and their blocks in ascending order; they are written to the
+ *   table and cleared in d_free_out;
+ *   for token t of row r: d_positions[t] = past[r] + t - cu[r], and d_token_slots[t] = page *
+ *   page_size + position % page_size;  for t from the total up to T: 0 and -1.
+ * cu_seqlens and seq_start are what engram_compress_hash takes.  A row of length 0 with no new
+ * token is a place that is not in use.
+ *   d_past, d_new, d_lens int32 [R] (d_lens may be d_past); R <= 8,192
+ *   d_tables int32 [R][table_ld], columns < max_blocks used
+ *   d_free_out may be d_free, or receives the whole bitmap and leaves d_free as it was
+ *   T: entries of d_positions and d_token_slots, at least the tokens of the call
+ *   d_seq_start, d_lens, d_positions may be NULL; d_positions and d_token_slots both when T = 0
+ * Host errors: ENGRAM_E_ARG, ENGRAM_E_ALIGN, ENGRAM_E_UNSUPPORTED.  Device errors:
+ * ENGRAM_E_SEQLENS (a negative length, a row past its max_blocks, more tokens than T),
+ * ENGRAM_E_PAGES; after either no page is taken and every row counts as bringing nothing.
+ * ENGRAM_E_PAGE_RANGE (an earlier entry that a new token lies in; its slot is -1). */
+int engram_block_plan(const int32_t* d_past, const int32_t* d_new, int32_t R, int32_t page_size, int32_t* d_tables,
+                      int64_t table_ld, int32_t max_blocks, const uint32_t* d_free, uint32_t* d_free_out,
+                      int32_t num_pages, int32_t* d_cu_seqlens, uint8_t* d_seq_start, int32_t* d_lens, int32_t T,
+                      int32_t* d_positions, int64_t* d_token_slots, hipStream_t stream);
+
+/* The pages of the first ceil(d_lens[r] / page_size) blocks of every row with d_flags[r] != 0
+ * become free.  Rows that share pages (beams of one request) are released in one call or
+ * after the last one that needs them.  Tables and lengths are left as they are.
+ * Host errors: ENGRAM_E_ARG, ENGRAM_E_ALIGN, ENGRAM_E_UNSUPPORTED.  Device errors:
+ * ENGRAM_E_SEQLENS (a length outside [0, max_blocks * page_size]; that row is left),
+ * ENGRAM_E_PAGE_RANGE (that entry is left). */
+int engram_block_release(const int32_t* d_tables, int64_t table_ld, int32_t max_blocks, const int32_t* d_lens,
+                         const uint8_t* d_flags, int32_t R, int32_t page_size, uint32_t* d_free, int32_t num_pages,
+                         hipStream_t stream);
+
+/* Beam search's selection.  Request g has K beams with total scores d_scores[g][b] and the
+ * next token's logits x[g][b][v] = d_logits[(g K + b) ld + v], v < V:
+ *   total(b, v) = scores[g][b] + x[g][b][v] - log sum over u of exp(x[g][b][u]).
+ * The n largest of a request's K * V totals, in descending order, equal ones by beam and within
+ * a beam by logit, then token:
+ *   d_tokens[g][i] = v, d_parents[g][i] = b, d_out_scores[g][i] = total rounded to float,
+ *   d_out_done[g][i] = 1 where v = end_token or the beam was done, else 0.
+ * A done beam (d_done[g][b] != 0) has ended: its logits are not read, its one candidate is
+ * end_token with its score unchanged.  No candidates: a logit of -inf; a beam whose score is
+ * not finite (its logits are not read), or whose logits hold a NaN or +inf, or are all -inf.
+ * Where a request has fewer than n candidates the rest is token -1, parent -1, score -inf,
+ * done 0.  Exponentials and their sums over a lane's part of the vocabulary are fp32, all sums
+ * above fp32 pairs and the totals 64 bits, so that totals are off by about 1e-7 times the
+ * logits' spread before their one rounding.
+ *   BF16 or F32 logits, rows aligned to their element, ld >= V,
+ *   1 <= V <= 2^24, 1 <= K, n <= 64, G >= 0, G * K <= 2^20; d_done and d_out_done may be NULL;
+ *   end_token in [0, V), or -1 for none (d_done then NULL); out_scores may be the scores and
+ *   out_done the done when n = K.
+ *   d_work: engram_beam_select_workspace(G, K, V, n) bytes, 16-byte aligned; calls that may run
+ *   at the same time need one each.
+ * Host errors: ENGRAM_E_ARG, ENGRAM_E_ALIGN, ENGRAM_E_SCRATCH, ENGRAM_E_UNSUPPORTED. */
+int engram_beam_select_workspace(int32_t G, int32_t K, int32_t V, int32_t n, int64_t* bytes);
+int engram_beam_select(const void* d_logits, int32_t logits_dtype, int64_t ld, int32_t G, int32_t K, int32_t V,
+                       const float* d_scores, const uint8_t* d_done, int32_t end_token, int32_t n, int32_t* d_tokens,
+                       int32_t* d_parents, float* d_out_scores, uint8_t* d_out_done, void* d_work, int64_t work_bytes,
+                       hipStream_t stream);
+
+/* States follow the selection: child c of request g's K beams continues its beam
+ * d_parents[g][c], or nothing (-1).  A beam's first child is its heir, which takes over what
+ * the beam alone writes to, its slot and its last, partly filled page; the other children (and
+ * those of no parent) take those of the beams without children, in ascending order, and the
+ * rows to copy into them are named.  So no row that is copied from is copied to, and beams keep
+ * distinct slots.  With h(c) the beam that child c takes over and p(c) its parent (h(c) where
+ * it has none):
+ *   slots (d_slots not NULL): slots_out[g][c] = slots[g][h(c)]; where p(c) != h(c), (slot_src,
+ *     slot_dst)[g][c] = (slots[g][p(c)], slots[g][h(c)]), else (-1, -1), also where either slot
+ *     is negative.  With a store, its three ids are copied so in this call ([VeOmni#1370]
+ *     decode-cache snapshot review: bounded state is copied).
+ *   tables (d_tables not NULL): row g K + c of tables_out = row p(c) of the group in its full
+ *     blocks (b < len / page_size), shared by all children; block len / page_size, when partly
+ *     filled, is that of h(c), and (page_src, page_dst)[g][c] = (that of p(c), that of h(c))
+ *     where they differ, else (-1, -1).  Pages of full blocks that a row of the group named
+ *     and none names any more become free in d_free (NULL: none does).  Columns from
+ *     ceil(len / page_size) on are left as they were.
+ * All beams of a request have the same length d_lens[g K .. g K + K - 1], and each names a
+ * partly filled page of its own; full blocks that are yet to be shared may be -1 in rows
+ * that are no parent.  Pages are shared inside a request only.
+ *   d_parents, d_slots, d_slot_src / dst, d_page_src / dst int32 [G][K]; K <= 64; d_tables
+ *   int32 [G * K][table_ld]; slots_out may be slots and tables_out tables (in place), else
+ *   they do not overlap; pairs may be NULL; store may be NULL (slots are then any numbers).
+ * Host errors: ENGRAM_E_ARG (also a store of another device), ENGRAM_E_ALIGN,
+ * ENGRAM_E_UNSUPPORTED.  Device errors: ENGRAM_E_PARENT_RANGE, ENGRAM_E_SEQLENS (unequal
+ * lengths or one outside its table; its rows of tables_out are not written): that request's
+ * beams all stay where they are;
+ * ENGRAM_E_SLOT_RANGE (that slot's store entry is left), ENGRAM_E_PAGE_RANGE (that page is not
+ * freed or that pair is -1). */
+int engram_beam_reorder(const int32_t* d_parents, int32_t G, int32_t K, engram_store* store, const int32_t* d_slots,
+                        int32_t* d_slots_out, int32_t* d_slot_src, int32_t* d_slot_dst, const int32_t* d_tables,
+                        int32_t* d_tables_out, int64_t table_ld, int32_t max_blocks, const int32_t* d_lens,
+                        int32_t page_size, uint32_t* d_free, int32_t num_pages, int32_t* d_page_src,
+                        int32_t* d_page_dst, hipStream_t stream);
+
+/* Rows of a state copied as named: for every pair i and plane q, row_bytes bytes of row
+ * d_src[i] -> row d_dst[i], row r of plane q at d_state + q * plane_pitch + r * row_pitch
+ * (a cache's pages in every layer, or slot-keyed states).  A pair with -1 on either side, or
+ * the same row on both, is none.  No row is a source and a destination, or a destination
+ * twice; engram_beam_reorder names such pairs.
+ *   planes, rows, n >= 0, rows < 2^31, planes * n < 2^24; 1 <= row_bytes < 2^26 - 1,024;
+ *   row_pitch >= row_bytes; plane_pitch >= 0.  A state whose address, pitches and row_bytes are multiples of 16 is copied fastest.
+ * Host errors: ENGRAM_E_ARG, ENGRAM_E_UNSUPPORTED.  Device error: ENGRAM_E_SLOT_RANGE (a row
+ * outside [0, rows): that pair is skipped). */
+int engram_state_copy(void* d_state, int64_t planes, int64_t plane_pitch, int64_t rows, int64_t row_pitch,
+                      int64_t row_bytes, const int32_t* d_src, const int32_t* d_dst, int32_t n, hipStream_t stream);
 
 /* ---- errors ------------------------------------------------------------- */
 const char* engram_strerror(int status);
