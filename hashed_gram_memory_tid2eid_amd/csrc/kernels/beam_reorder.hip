@@ -159,6 +159,7 @@ hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t stream) {
 // takes one piece of a long row, or a group of lanes each one short row.
 
 constexpr int kCopyThreads = 256;
+typedef uint32_t copy16_t __attribute__((ext_vector_type(4)));
 
 template <typename U>
 __global__ __launch_bounds__(kCopyThreads) void state_copy_kernel(StateCopyArgs a, uint32_t units, uint32_t lanes) {
@@ -197,7 +198,7 @@ hipError_t launch_state_copy(const StateCopyArgs& a, hipStream_t stream) {
   const uint64_t items = (uint64_t)a.n * (uint64_t)a.planes, per = kCopyThreads / lanes;
   const dim3 grid((unsigned)((items + per - 1) / per), (units + lanes * 4 - 1) / (lanes * 4));
   if (unit == 16)
-    hipLaunchKernelGGL(state_copy_kernel<uint4>, grid, dim3(kCopyThreads), 0, stream, a, units, lanes);
+    hipLaunchKernelGGL(state_copy_kernel<copy16_t>, grid, dim3(kCopyThreads), 0, stream, a, units, lanes);
   else if (unit == 4)
     hipLaunchKernelGGL(state_copy_kernel<uint32_t>, grid, dim3(kCopyThreads), 0, stream, a, units, lanes);
   else

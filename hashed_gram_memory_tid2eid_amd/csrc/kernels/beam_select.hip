@@ -7,18 +7,20 @@
 // bytes, one workgroup each, and reads each logit once: a piece stays in registers while its
 // maximum m is found, then its sum of exp(x - m) and its n largest logits.  Those need no sort
 // of the piece: lane i of the four waves stands for the maximum of its elements, and a bound
-// that n of these 64 maxima reach is reached by n elements at least and by few more, so the
-// elements that reach it go to a list in LDS, and each finds its rank by counting the larger
-// ones.  Keys of (logit, lowest token first) are all different, so ranks are, too, whatever
-// the order in which the list was filled.  A list that overflows (many equal logits) is not
-// used; the piece's n largest are then taken one by one.
+// that n of these 64 maxima reach is reached by n elements at least and by few more.  The loads
+// that hold such an element go to a list in LDS whole, the elements in them that reach the bound
+// to a second one, and there each finds its rank by counting the larger ones.  Keys of (logit,
+// lowest token first) are all different, so ranks are, too, whatever the order in which the
+// lists were filled.  Lists that overflow (many equal logits) are not used; the piece's n
+// largest are then taken one by one.
 // The second launch, one workgroup a request, adds the pieces' sums in 64 bits, turns the keys
 // into totals and selects among them by the same bound, list and count.
 
 namespace engram {
 
 constexpr int kSelectThreads = 256;
-constexpr int kSelectList = 1024;
+constexpr int kSelectLoads = 512;  // loads that hold an element which reaches the bound
+constexpr int kSelectList = 1024;  // such elements
 constexpr int kMergeList = 2048;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.44269504088896341f;
@@ -65,15 +67,15 @@ struct Logits<float> {
   typedef float raw_t __attribute__((ext_vector_type(4)));
   typedef raw_t anywhere_t __attribute__((aligned(4)));
   raw_t raw;
+  __device__ __forceinline__ void load(const float* x, int e) { raw = *reinterpret_cast<const anywhere_t*>(x + e); }
   __device__ __forceinline__ void load(const float* x, int e, int V) {
-    if (e + kVec <= V) {
-      raw = *reinterpret_cast<const anywhere_t*>(x + e);
-      return;
-    }
 #pragma unroll
     for (int i = 0; i < kVec; ++i) raw[i] = e + i < V ? x[e + i] : -INFINITY;
   }
   __device__ __forceinline__ float at(int i) const { return raw[i]; }
+  // at(i) for an i that is not known before, in LDS
+  __device__ __forceinline__ float pick(int i) const { return reinterpret_cast<const float*>(&raw)[i]; }
+  __device__ __forceinline__ void again() {}
 };
 template <>
 struct Logits<uint16_t> {  // bf16
@@ -81,11 +83,8 @@ struct Logits<uint16_t> {  // bf16
   typedef uint32_t raw_t __attribute__((ext_vector_type(4)));
   typedef raw_t anywhere_t __attribute__((aligned(2)));
   raw_t raw;
+  __device__ __forceinline__ void load(const uint16_t* x, int e) { raw = *reinterpret_cast<const anywhere_t*>(x + e); }
   __device__ __forceinline__ void load(const uint16_t* x, int e, int V) {
-    if (e + kVec <= V) {
-      raw = *reinterpret_cast<const anywhere_t*>(x + e);
-      return;
-    }
 #pragma unroll
     for (int i = 0; i < kVec; i += 2) {
       const uint32_t lo = e + i < V ? x[e + i] : 0xFF80u;
@@ -96,64 +95,102 @@ struct Logits<uint16_t> {  // bf16
   __device__ __forceinline__ float at(int i) const {
     return __uint_as_float(i & 1 ? raw[i / 2] & 0xFFFF0000u : raw[i / 2] << 16);
   }
+  __device__ __forceinline__ float pick(int i) const {
+    return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(&raw)[i] << 16);
+  }
+  // Widened logits are not kept from one pass to the next: 64 registers instead of 32 would cost
+  // half of the waves.
+  __device__ __forceinline__ void again() { asm volatile("" : "+v"(raw)); }
 };
+
+__device__ __forceinline__ float one_logit(const float* x, int e) { return x[e]; }
+__device__ __forceinline__ float one_logit(const uint16_t* x, int e) { return __uint_as_float((uint32_t)x[e] << 16); }
+
+// What a piece whose maximum is m takes off its exponents (in powers of two).
+constexpr float kFar = 1099511627776.0f;  // 2^40
+__device__ __forceinline__ float select_center(float m) { return fabsf(m) < kFar ? m * kLog2e : 0.0f; }
 
 // Beams whose logits are not read: done, or without a finite score.
 __device__ __forceinline__ bool beam_is_live(const SelectArgs& a, int row) {
   return (a.done == nullptr || a.done[row] == 0) && isfinite(a.scores[row]);
 }
 
+// (8 waves a SIMD: 64 registers, and 8 workgroups' lists fit a CU's LDS)
 template <typename T, int NV>
-__global__ __launch_bounds__(kSelectThreads) void beam_select_rows_kernel(SelectArgs a) {
+__global__ __launch_bounds__(kSelectThreads, 8) void beam_select_rows_kernel(SelectArgs a) {
   constexpr int kVec = Logits<T>::kVec;
   const int row = (int)(blockIdx.x / (unsigned)a.splits), piece = (int)(blockIdx.x % (unsigned)a.splits);
   if (!beam_is_live(a, row)) return;
   __shared__ float lane_max[4][64];
   __shared__ float wave_sum[4];
+  __shared__ Logits<T> load_list[kSelectLoads];
+  __shared__ int load_at[kSelectLoads];
   __shared__ unsigned long long list[kSelectList];
-  __shared__ int listed;
+  __shared__ int loads, listed;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const T* x = static_cast<const T*>(a.logits) + row * a.ld;
-  const int e0 = (piece * NV * kSelectThreads + tid) * kVec;
+  const int first = piece * NV * kSelectThreads * kVec, end = min(a.V, first + NV * kSelectThreads * kVec);
+  const int e0 = first + tid * kVec;
   Logits<T> v[NV];
+  if (end - first == NV * kSelectThreads * kVec) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) v[j].load(x, e0 + j * kSelectThreads * kVec, a.V);
-  if (tid == 0) listed = 0;
+    for (int j = 0; j < NV; ++j) v[j].load(x, e0 + j * kSelectThreads * kVec);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int e = e0 + j * kSelectThreads * kVec;
+      if (e + kVec <= end)
+        v[j].load(x, e);
+      else
+        v[j].load(x, e, end);
+    }
+  }
+  if (tid == 0) loads = listed = 0;
 
-  float most[NV];  // of each load: most of them reach no bound and are passed over whole
+  // a NaN makes its maxima NaN, +inf infinite: rows without candidates
+  float most[NV];
   float mine = -INFINITY;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     most[j] = v[j].at(0);
 #pragma unroll
-    for (int i = 1; i < kVec; ++i) most[j] = fmaxf(most[j], v[j].at(i));
-    mine = fmaxf(mine, most[j]);
+    for (int i = 1; i < kVec; ++i) most[j] = __builtin_elementwise_maximum(most[j], v[j].at(i));
+    mine = __builtin_elementwise_maximum(mine, most[j]);
+    v[j].again();
   }
   lane_max[wave][lane] = mine;
   __syncthreads();
-  const float of_lane = fmaxf(fmaxf(lane_max[0][lane], lane_max[1][lane]), fmaxf(lane_max[2][lane], lane_max[3][lane]));
+  const float of_lane = __builtin_elementwise_maximum(
+      __builtin_elementwise_maximum(lane_max[0][lane], lane_max[1][lane]),
+      __builtin_elementwise_maximum(lane_max[2][lane], lane_max[3][lane]));
   float m = of_lane;
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  for (int off = 32; off >= 1; off >>= 1) m = __builtin_elementwise_maximum(m, __shfl_xor(m, off, 64));
   // the bound keeps 16 bits: exact for bf16, and 2^-8 below the n-th of the maxima for fp32
   const uint32_t reach = bound_of_lanes(in_order(of_lane), a.n, 16);
   const float bound = reach <= in_order(kLowest) ? kLowest : from_order(reach);
 
-  // exp(x - m) as a power of two; an infinity or a NaN among the logits makes the sum a NaN
-  const float base = m == -INFINITY ? 0.0f : m;
+  // exp(x - m) as 2^(x log2e - c), c the float next to m log2e: one fma, rounded by 2^-24 of the
+  // exponent; the merge makes up for c's own rounding.  (Far from zero only x = m counts: the
+  // next float is 2^16 or more away.)
+  const float c = select_center(m);
+  const bool far = fabsf(m) >= kFar;
   float sum[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) sum[i & 1] += __builtin_amdgcn_exp2f((v[j].at(i) - base) * kLog2e);
     if (most[j] >= bound) {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        if (v[j].at(i) >= bound) {
-          const int place = atomicAdd(&listed, 1);
-          if (place < kSelectList) list[place] = select_key(v[j].at(i), e0 + j * kSelectThreads * kVec + i);
-        }
+      const int place = atomicAdd(&loads, 1);
+      if (place < kSelectLoads) {
+        load_list[place] = v[j];
+        load_at[place] = e0 + j * kSelectThreads * kVec;
       }
+    }
+    if (!far) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) sum[i & 1] += __builtin_amdgcn_exp2f(__builtin_fmaf(v[j].at(i), kLog2e, -c));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) sum[i & 1] += v[j].at(i) == m ? 1.0f : 0.0f;
     }
   }
   float s = sum[0] + sum[1];
@@ -161,12 +198,19 @@ __global__ __launch_bounds__(kSelectThreads) void beam_select_rows_kernel(Select
   for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off, 64);
   if (lane == 0) wave_sum[wave] = s;
   __syncthreads();
-  if (tid == 0) {
-    a.parts[blockIdx.x] = make_float2(m, (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]));
+  if (tid == 0) a.parts[blockIdx.x] = make_float2(m, (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]));
+  const int held = min(loads, kSelectLoads) * kVec;
+  for (int i = tid; i < held; i += kSelectThreads) {
+    const float f = load_list[i / kVec].pick(i % kVec);
+    if (f >= bound) {
+      const int place = atomicAdd(&listed, 1);
+      if (place < kSelectList) list[place] = select_key(f, load_at[i / kVec] + i % kVec);
+    }
   }
+  __syncthreads();
   unsigned long long* out = a.keys + (int64_t)blockIdx.x * a.n;
   const int count = listed;
-  if (count <= kSelectList) {
+  if (loads <= kSelectLoads && count <= kSelectList) {
     for (int i = tid; i < count; i += kSelectThreads) {
       const unsigned long long key = list[i];
       int rank = 0;
@@ -176,19 +220,15 @@ __global__ __launch_bounds__(kSelectThreads) void beam_select_rows_kernel(Select
     for (int i = count + tid; i < a.n; i += kSelectThreads) out[i] = 0;
     return;
   }
-  // too many equal ones: one by one, each the largest key below the last
+  // too many equal ones: one by one from memory, each the largest key below the last
   __shared__ unsigned long long wave_best[4];
   unsigned long long last = ~0ull;
   for (int r = 0; r < a.n; ++r) {
     unsigned long long best = 0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const float f = v[j].at(i);
-        const unsigned long long key = select_key(f, e0 + j * kSelectThreads * kVec + i);
-        if (f >= kLowest && key < last && key > best) best = key;
-      }
+    for (int e = first + tid; e < end; e += kSelectThreads) {
+      const float f = one_logit(x, e);
+      const unsigned long long key = select_key(f, e);
+      if (f >= kLowest && key < last && key > best) best = key;
     }
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) {
@@ -220,6 +260,9 @@ __device__ __forceinline__ bool goes_before(double ta, int ba, unsigned long lon
   return ta > tb || (ta == tb && (ba < bb || (ba == bb && ka > kb)));
 }
 
+// Keys a thread keeps in registers.
+constexpr int kMergeKeys = 8;
+
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a) {
   __shared__ MergeBeams beams;
@@ -230,28 +273,42 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
   __shared__ int listed;
   const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int S = a.splits, K = a.K, n = a.n;
+  // place i of the request's keys is the (i / pieces)-th of piece i % pieces, so that the lanes
+  // share the pieces' first keys evenly
+  const int pieces = K * S, places = pieces * n;
+  const unsigned long long* all = a.keys + (int64_t)g * places;
+  auto key_at = [&](int i) { return all[(i % pieces) * n + i / pieces]; };
+  unsigned long long mine[kMergeKeys];  // (of beams that are not live: not written, and not looked at)
+#pragma unroll
+  for (int q = 0; q < kMergeKeys; ++q) mine[q] = tid + q * THREADS < places ? key_at(tid + q * THREADS) : 0;
   if (tid == 0) listed = 0;
   for (int b = wave; b < K; b += THREADS / 64) {
     const int row = g * K + b;
+    const float2* part = a.parts + (int64_t)row * S;
+    float2 p = lane < S ? part[lane] : make_float2(-INFINITY, 0.0f);
     const float score = a.scores[row];
     int kind = !isfinite(score) ? 0 : a.done != nullptr && a.done[row] != 0 ? 2 : 1;
     double most = 0.0, norm = 0.0;
     if (kind == 1) {
-      const float2* part = a.parts + (int64_t)row * S;
-      float m = -INFINITY;
-      for (int i = lane; i < S; i += 64) m = fmaxf(m, part[i].x);
+      float m = p.x;
+      for (int i = lane + 64; i < S; i += 64) m = __builtin_elementwise_maximum(m, part[i].x);
 #pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+      for (int off = 32; off >= 1; off >>= 1) m = __builtin_elementwise_maximum(m, __shfl_xor(m, off, 64));
+      kind = 0;
       if (isfinite(m)) {
         double z = 0.0;
-        for (int i = lane; i < S; i += 64) z += (double)part[i].y * exp((double)part[i].x - (double)m);
+        for (int i = lane; i < S; i += 64) {
+          if (i >= 64) p = part[i];
+          // a piece's sum is of 2^(x log2e - c), with the constant as fp32 has it
+          const double shift = (double)select_center(p.x) - (fabsf(p.x) < kFar ? (double)p.x * (double)kLog2e : 0.0);
+          const float scale = __builtin_amdgcn_exp2f((p.x - m) * kLog2e);
+          z += (double)p.y * (double)scale * (1.0 + shift * 0.6931471805599453);
+        }
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) z += __shfl_xor(z, off, 64);
         most = (double)m;
         norm = log(z);
-        if (!(z == z)) kind = 0;
-      } else {
-        kind = 0;
+        if (isfinite(z)) kind = 1;
       }
     }
     if (lane == 0) {
@@ -263,22 +320,29 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
   }
   __syncthreads();
 
-  // a bound that n of 64 lanes reach with the first, largest, key of their pieces
-  const int pieces = K * S;
-  const unsigned long long* all = a.keys + (int64_t)g * pieces * n;
-  uint32_t mine = 0;
-  for (int l = tid; l < pieces; l += THREADS) {
-    const int b = l / S;
-    if (beams.kind[b] != 1) continue;
-    const unsigned long long key = all[(int64_t)l * n];
-    if (key != 0) mine = max(mine, high_in_order(beam_total(beams, b, key)));
+  // a bound that n of 64 lanes reach, by the 13 leading bits of the totals' mantissas
+  auto total_at = [&](int i, unsigned long long key, int* b) {
+    *b = i % pieces / S;
+    return beam_total(beams, *b, key);
+  };
+  uint32_t top = 0;
+  uint32_t high[kMergeKeys];
+#pragma unroll
+  for (int q = 0; q < kMergeKeys; ++q) {
+    high[q] = 0;
+    const int i = tid + q * THREADS;
+    if (i >= places) continue;
+    int b;
+    const double total = total_at(i, mine[q], &b);
+    if (beams.kind[b] == 1 && mine[q] != 0) high[q] = high_in_order(total);
+    top = max(top, high[q]);
   }
-  lane_max[tid] = mine;
+  lane_max[tid] = top;
   __syncthreads();
   uint32_t of_lane = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 64; ++w) of_lane = max(of_lane, lane_max[w * 64 + lane]);
-  const uint32_t bound = bound_of_lanes(of_lane, n, 32);
+  const uint32_t bound = max(1u, bound_of_lanes(of_lane, n, 24));
 
   auto push = [&](double total, int b, unsigned long long key) {
     const int place = atomicAdd(&listed, 1);
@@ -288,17 +352,19 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
       of_beam[place] = (uint8_t)b;
     }
   };
-  const bool many = (int64_t)pieces * n > 8 * THREADS;  // then a piece's first key says whether to look at the others
-  for (int64_t i = tid; i < (int64_t)pieces * n; i += THREADS) {
-    const int l = (int)(i / n), b = l / S;
+#pragma unroll
+  for (int q = 0; q < kMergeKeys; ++q) {
+    if (high[q] < bound) continue;
+    int b;
+    const double total = total_at(tid + q * THREADS, mine[q], &b);
+    push(total, b, mine[q]);
+  }
+  for (int i = tid + kMergeKeys * THREADS; i < places; i += THREADS) {
+    int b = i % pieces / S;
     if (beams.kind[b] != 1) continue;
-    if (many) {
-      const unsigned long long head = all[(int64_t)l * n];
-      if (head == 0 || high_in_order(beam_total(beams, b, head)) < bound) continue;
-    }
-    const unsigned long long key = all[i];
+    const unsigned long long key = key_at(i);
     if (key == 0) continue;
-    const double total = beam_total(beams, b, key);
+    const double total = total_at(i, key, &b);
     if (high_in_order(total) >= bound) push(total, b, key);
   }
   if (tid < K && beams.kind[tid] == 2) push(beams.score[tid], tid, select_key(0.0f, a.end_token));
@@ -349,8 +415,8 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
         best_b = b;
       }
     };
-    for (int64_t i = tid; i < (int64_t)pieces * n; i += THREADS) {
-      const int b = (int)(i / n) / S;
+    for (int i = tid; i < places; i += THREADS) {
+      const int b = i / n / S;
       if (beams.kind[b] != 1) continue;
       const unsigned long long key = all[i];
       if (key != 0) consider(beam_total(beams, b, key), b, key);
@@ -454,10 +520,10 @@ hipError_t launch_beam_select(const SelectArgs& args, hipStream_t stream) {
     launch_select_rows<uint16_t>(a, nv, stream);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if ((int64_t)a.K * a.splits * a.n > 4096)
+  if ((int64_t)a.K * a.splits * a.n > kMergeKeys * 512)
     hipLaunchKernelGGL(beam_select_merge_kernel<1024>, dim3(a.G), dim3(1024), 0, stream, a);
   else
-    hipLaunchKernelGGL(beam_select_merge_kernel<256>, dim3(a.G), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(beam_select_merge_kernel<512>, dim3(a.G), dim3(512), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -289,10 +289,11 @@ def run_select(x, scores, done, end, n, dtype, *, ld=None, offset=0, in_place=Fa
 
 def check_select(x, scores, done, end, n, dtype, **how):
     """Totals: a rounding to float (2^-24) of score + (x - most) - norm, where norm's error is that of
-    the exponentials: x - most and its product with log2(e) are rounded (2^-24 |x - most| each, the
-    constant's 2^-26 and log2's unit of the instruction beside them: under 2.5 x 2^-24 |x - most|
-    + 2 x 2^-24), and of the fp32 sums of one lane (at most 32 terms an accumulator), its two
-    accumulators, a wave (6 steps) and four waves (2): 41 x 2^-24.  All terms are positive, so norm
+    the exponentials: a difference to the largest logit and its product with log2(e) are rounded
+    (2^-24 |x - most| each at most, the constant's 2^-26 and the unit of the exponential itself
+    beside them: under 2.5 x 2^-24 |x - most| + 2 x 2^-24), and of the fp32 sums of one lane (at
+    most 32 terms an accumulator), its two accumulators, a wave (6 steps) and four waves (2):
+    41 x 2^-24.  All terms are positive, so norm
     is off by their weighted mean, at most by the largest.  |x - most| counts at most to 104, where
     exp leaves fp32's range."""
     x = torch.as_tensor(x).to(dtype).double().numpy()
