@@ -325,7 +325,8 @@ struct PlanArgs {
   int32_t T;
   int32_t* positions;    // [T] or null
   int64_t* token_slots;  // [T] or null
-  int32_t granule_words; // set by the launcher: words of the bitmap counted together
+  int64_t stretch;       // set by the launcher: words of the bitmap that are counted together
+  uint32_t page_inverse; // set by the launcher: floor((2^32 - 1) / page_size)
   int32_t tokens_here;   // set by the launcher: tokens are done by the planning workgroup
 };
 hipError_t launch_block_plan(const PlanArgs& a, hipStream_t stream);

@@ -19,8 +19,9 @@
 namespace engram {
 
 constexpr int kSelectThreads = 256;
-constexpr int kSelectLoads = 512;  // loads that hold an element which reaches the bound
-constexpr int kSelectList = 1024;  // such elements
+constexpr int kSelectHeld = 4096;  // elements of the loads that hold one which reaches the bound
+constexpr int kSelectList = 1024;  // elements that reach it
+constexpr int kRankLanes = 8;      // lanes that count the larger ones of one element together
 constexpr int kMergeList = 2048;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.44269504088896341f;
@@ -63,11 +64,11 @@ template <typename T>
 struct Logits;
 template <>
 struct Logits<float> {
-  static constexpr int kVec = 4;
+  static constexpr int kVec = 4, kWaves = 5;
   typedef float raw_t __attribute__((ext_vector_type(4)));
   typedef raw_t anywhere_t __attribute__((aligned(4)));
   raw_t raw;
-  __device__ __forceinline__ void load(const float* x, int e) { raw = *reinterpret_cast<const anywhere_t*>(x + e); }
+  __device__ __forceinline__ void load(const float* x, int e) { raw = __builtin_nontemporal_load(reinterpret_cast<const anywhere_t*>(x + e)); }
   __device__ __forceinline__ void load(const float* x, int e, int V) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) raw[i] = e + i < V ? x[e + i] : -INFINITY;
@@ -79,11 +80,11 @@ struct Logits<float> {
 };
 template <>
 struct Logits<uint16_t> {  // bf16
-  static constexpr int kVec = 8;
+  static constexpr int kVec = 8, kWaves = 8;
   typedef uint32_t raw_t __attribute__((ext_vector_type(4)));
   typedef raw_t anywhere_t __attribute__((aligned(2)));
   raw_t raw;
-  __device__ __forceinline__ void load(const uint16_t* x, int e) { raw = *reinterpret_cast<const anywhere_t*>(x + e); }
+  __device__ __forceinline__ void load(const uint16_t* x, int e) { raw = __builtin_nontemporal_load(reinterpret_cast<const anywhere_t*>(x + e)); }
   __device__ __forceinline__ void load(const uint16_t* x, int e, int V) {
 #pragma unroll
     for (int i = 0; i < kVec; i += 2) {
@@ -115,10 +116,13 @@ __device__ __forceinline__ bool beam_is_live(const SelectArgs& a, int row) {
   return (a.done == nullptr || a.done[row] == 0) && isfinite(a.scores[row]);
 }
 
-// (8 waves a SIMD: 64 registers, and 8 workgroups' lists fit a CU's LDS)
+// Logits are read past the caches (2,048 rows of 129,280 fp32: 175 -> 157 us).  bf16 is bound
+// by its exponentials and runs 8 waves a SIMD: 64 registers, and 8 workgroups' lists in a CU's
+// LDS; fp32 by memory, where 5 workgroups, which is what its lists leave, read faster than 8
+// (154 against 157 us; bf16, 512 rows of 65,537: 26 against 24).
 template <typename T, int NV>
-__global__ __launch_bounds__(kSelectThreads, 8) void beam_select_rows_kernel(SelectArgs a) {
-  constexpr int kVec = Logits<T>::kVec;
+__global__ __launch_bounds__(kSelectThreads, Logits<T>::kWaves) void beam_select_rows_kernel(SelectArgs a) {
+  constexpr int kVec = Logits<T>::kVec, kSelectLoads = kSelectHeld / kVec;
   const int row = (int)(blockIdx.x / (unsigned)a.splits), piece = (int)(blockIdx.x % (unsigned)a.splits);
   if (!beam_is_live(a, row)) return;
   __shared__ float lane_max[4][64];
@@ -211,11 +215,13 @@ __global__ __launch_bounds__(kSelectThreads, 8) void beam_select_rows_kernel(Sel
   unsigned long long* out = a.keys + (int64_t)blockIdx.x * a.n;
   const int count = listed;
   if (loads <= kSelectLoads && count <= kSelectList) {
-    for (int i = tid; i < count; i += kSelectThreads) {
+    for (int i = tid / kRankLanes; i < count; i += kSelectThreads / kRankLanes) {
       const unsigned long long key = list[i];
       int rank = 0;
-      for (int k = 0; k < count; ++k) rank += list[k] > key ? 1 : 0;
-      if (rank < a.n) out[rank] = key;
+      for (int k = tid % kRankLanes; k < count; k += kRankLanes) rank += list[k] > key ? 1 : 0;
+#pragma unroll
+      for (int off = kRankLanes / 2; off >= 1; off >>= 1) rank += __shfl_xor(rank, off, 64);
+      if (rank < a.n && tid % kRankLanes == 0) out[rank] = key;
     }
     for (int i = count + tid; i < a.n; i += kSelectThreads) out[i] = 0;
     return;
@@ -277,10 +283,23 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
   // share the pieces' first keys evenly
   const int pieces = K * S, places = pieces * n;
   const unsigned long long* all = a.keys + (int64_t)g * places;
-  auto key_at = [&](int i) { return all[(i % pieces) * n + i / pieces]; };
   unsigned long long mine[kMergeKeys];  // (of beams that are not live: not written, and not looked at)
+  int piece_of[kMergeKeys];
+  {
+    int piece = tid % pieces, order = tid / pieces;
+    const int step = THREADS % pieces, steps = THREADS / pieces;
 #pragma unroll
-  for (int q = 0; q < kMergeKeys; ++q) mine[q] = tid + q * THREADS < places ? key_at(tid + q * THREADS) : 0;
+    for (int q = 0; q < kMergeKeys; ++q) {
+      piece_of[q] = piece;
+      mine[q] = order < n ? all[piece * n + order] : 0;
+      piece += step;
+      order += steps;
+      if (piece >= pieces) {
+        piece -= pieces;
+        ++order;
+      }
+    }
+  }
   if (tid == 0) listed = 0;
   for (int b = wave; b < K; b += THREADS / 64) {
     const int row = g * K + b;
@@ -320,29 +339,26 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
   }
   __syncthreads();
 
-  // a bound that n of 64 lanes reach, by the 13 leading bits of the totals' mantissas
-  auto total_at = [&](int i, unsigned long long key, int* b) {
-    *b = i % pieces / S;
-    return beam_total(beams, *b, key);
-  };
+  // a bound that n of 64 lanes reach, by the 12 leading bits of the totals' mantissas
+  double total[kMergeKeys];
   uint32_t top = 0;
-  uint32_t high[kMergeKeys];
 #pragma unroll
   for (int q = 0; q < kMergeKeys; ++q) {
-    high[q] = 0;
-    const int i = tid + q * THREADS;
-    if (i >= places) continue;
-    int b;
-    const double total = total_at(i, mine[q], &b);
-    if (beams.kind[b] == 1 && mine[q] != 0) high[q] = high_in_order(total);
-    top = max(top, high[q]);
+    if (mine[q] == 0) continue;
+    piece_of[q] /= S;  // the beam
+    if (beams.kind[piece_of[q]] != 1) {
+      mine[q] = 0;
+      continue;
+    }
+    total[q] = beam_total(beams, piece_of[q], mine[q]);
+    top = max(top, high_in_order(total[q]));
   }
   lane_max[tid] = top;
   __syncthreads();
   uint32_t of_lane = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 64; ++w) of_lane = max(of_lane, lane_max[w * 64 + lane]);
-  const uint32_t bound = max(1u, bound_of_lanes(of_lane, n, 24));
+  const uint32_t bound = bound_of_lanes(of_lane, n, 24);
 
   auto push = [&](double total, int b, unsigned long long key) {
     const int place = atomicAdd(&listed, 1);
@@ -353,19 +369,15 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
     }
   };
 #pragma unroll
-  for (int q = 0; q < kMergeKeys; ++q) {
-    if (high[q] < bound) continue;
-    int b;
-    const double total = total_at(tid + q * THREADS, mine[q], &b);
-    push(total, b, mine[q]);
-  }
+  for (int q = 0; q < kMergeKeys; ++q)
+    if (mine[q] != 0 && high_in_order(total[q]) >= bound) push(total[q], piece_of[q], mine[q]);
   for (int i = tid + kMergeKeys * THREADS; i < places; i += THREADS) {
-    int b = i % pieces / S;
+    const int piece = i % pieces, b = piece / S;
     if (beams.kind[b] != 1) continue;
-    const unsigned long long key = key_at(i);
+    const unsigned long long key = all[piece * n + i / pieces];
     if (key == 0) continue;
-    const double total = total_at(i, key, &b);
-    if (high_in_order(total) >= bound) push(total, b, key);
+    const double t = beam_total(beams, b, key);
+    if (high_in_order(t) >= bound) push(t, b, key);
   }
   if (tid < K && beams.kind[tid] == 2) push(beams.score[tid], tid, select_key(0.0f, a.end_token));
   __syncthreads();
@@ -387,13 +399,16 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
   };
   const int count = listed;
   if (count <= kMergeList) {
-    for (int i = tid; i < count; i += THREADS) {
+    for (int i = tid / kRankLanes; i < count; i += THREADS / kRankLanes) {
       const double total = totals[i];
       const unsigned long long key = keys[i];
       const int b = of_beam[i];
       int rank = 0;
-      for (int k = 0; k < count; ++k) rank += goes_before(totals[k], of_beam[k], keys[k], total, b, key) ? 1 : 0;
-      if (rank < n) write(rank, total, b, key);
+      for (int k = tid % kRankLanes; k < count; k += kRankLanes)
+        rank += goes_before(totals[k], of_beam[k], keys[k], total, b, key) ? 1 : 0;
+#pragma unroll
+      for (int off = kRankLanes / 2; off >= 1; off >>= 1) rank += __shfl_xor(rank, off, 64);
+      if (rank < n && tid % kRankLanes == 0) write(rank, total, b, key);
     }
     for (int r = count + tid; r < n; r += THREADS) write_none(r);
     return;

@@ -12,47 +12,54 @@ import ctypes
 
 import torch
 
-from . import _check, _lib, _need
-from .train_ops import _INT, _WIDE, _flat, _launch_stream, _matrix, _work
+from . import _check, _dev, _lib, _need, _stream
+from .train_ops import _INT, _WIDE, _matrix
 
-_I32, _U8 = torch.int32, torch.uint8
+_I32, _I64, _U8, _F32 = torch.int32, torch.int64, torch.uint8, torch.float32
 
 
-def _serve_stream(stream, *tensors):
-    """The raw stream of a call whose tensors must all live on the current device."""
-    raw = _launch_stream(stream, *tensors)
-    for t in tensors:
-        if t is not None:
-            if t.get_device() != torch.cuda.current_device():
-                raise ValueError(f"tensors on device {t.get_device()}, the current device is {torch.cuda.current_device()}")
-            break
-    return raw
+def _place(t, name):
+    """The device of a call, which is that of its tensors and the current one."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    dev = t.get_device()
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on device {dev}, the current device is {torch._C._cuda_getDevice()}")
+    return dev
+
+
+def _raw(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _arg(t, name, dtype, least, dev):
+    """Pointer of a contiguous tensor of at least so many elements on the call's device, or None."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.numel() >= least and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, name)  # says what is wrong, if it is one of these
+    _need(t.numel() >= least, f"{name} too small")
+    raise ValueError(f"{name} is on device {t.get_device()}, the call on device {dev}")
 
 
 def _count(n, name):
     """A whole number that a 32-bit argument holds."""
     n = int(n)
-    _need(0 <= n < 1 << 31, f"{name} must be in [0, 2^31), got {n}")
+    if not 0 <= n < 1 << 31:
+        raise ValueError(f"{name} must be in [0, 2^31), got {n}")
     return n
 
 
-def _of(t, name, dtype, least):
-    """Pointer of a contiguous device tensor of at least so many elements, or None."""
-    if t is None:
-        return None
-    p = _flat(t, name, dtype)
-    _need(t.numel() >= least, f"{name} too small")
-    return p
-
-
-def _tables(t, name, rows):
+def _tables(t, name, rows, dev):
+    """(pointer, columns, leading dimension) of a table of so many rows."""
     p, n, blocks, ld, _ = _matrix(t, name, _INT)
     _need(n == rows, f"{name} must have {rows} rows")
+    _need(t.get_device() == dev, f"{name} is on another device")
     return p, blocks, ld
-
-
-def _pool(free, name, num_pages):
-    return _of(free, name, _I32, (num_pages + 31) // 32)
 
 
 def engram_block_plan(past, new, tables, free, *, page_size, num_pages, cu_seqlens, token_slots, positions=None,
@@ -61,29 +68,31 @@ def engram_block_plan(past, new, tables, free, *, page_size, num_pages, cu_seqle
     [R][blocks] (updated); free the pool (updated, or left as it is with free_out, which
     receives it).  Writes cu_seqlens [R + 1], token_slots int64 [T] and, where given, positions
     int32 [T], seq_start uint8 [R], lens int32 [R] (may be past); T is token_slots' size."""
+    dev = _place(past, "past")
     R, T = past.numel(), _count(token_slots.numel(), "T")
     page_size, num_pages = _count(page_size, "page_size"), _count(num_pages, "num_pages")
+    words = (num_pages + 31) // 32
     _need(new.numel() == R, "past and new must be of one size")
-    tp, blocks, ld = _tables(tables, "tables", R)
-    out = free if free_out is None else free_out
+    tp, blocks, ld = _tables(tables, "tables", R, dev)
+    fp = _arg(free, "free", _I32, words, dev)
     _check(_lib.engram_block_plan(
-        _of(past, "past", _I32, R), _of(new, "new", _I32, R), R, page_size, tp, ld, blocks, _pool(free, "free", num_pages),
-        _pool(out, "free_out", num_pages), num_pages, _of(cu_seqlens, "cu_seqlens", _I32, R + 1),
-        _of(seq_start, "seq_start", _U8, R), _of(lens, "lens", _I32, R), T, _of(positions, "positions", _I32, T),
-        _of(token_slots, "token_slots", torch.int64, T),
-        _serve_stream(stream, past, new, tables, free, out, cu_seqlens, seq_start, lens, positions, token_slots)),
-        "engram_block_plan")
+        _arg(past, "past", _I32, R, dev), _arg(new, "new", _I32, R, dev), R, page_size, tp, ld, blocks, fp,
+        fp if free_out is None else _arg(free_out, "free_out", _I32, words, dev), num_pages,
+        _arg(cu_seqlens, "cu_seqlens", _I32, R + 1, dev), _arg(seq_start, "seq_start", _U8, R, dev),
+        _arg(lens, "lens", _I32, R, dev), T, _arg(positions, "positions", _I32, T, dev),
+        _arg(token_slots, "token_slots", _I64, T, dev), _raw(stream, dev)), "engram_block_plan")
 
 
 def engram_block_release(tables, lens, flags, free, *, page_size, num_pages, stream=None):
     """The pages of rows with a flag become free: tables int32 [R][blocks], lens int32 [R],
     flags uint8 [R]; free is updated."""
+    dev = _place(lens, "lens")
     R = _count(lens.numel(), "R")
     page_size, num_pages = _count(page_size, "page_size"), _count(num_pages, "num_pages")
-    tp, blocks, ld = _tables(tables, "tables", R)
-    _check(_lib.engram_block_release(tp, ld, blocks, _of(lens, "lens", _I32, R), _of(flags, "flags", _U8, R), R, page_size,
-                                     _pool(free, "free", num_pages), num_pages,
-                                     _serve_stream(stream, tables, lens, flags, free)), "engram_block_release")
+    tp, blocks, ld = _tables(tables, "tables", R, dev)
+    _check(_lib.engram_block_release(
+        tp, ld, blocks, _arg(lens, "lens", _I32, R, dev), _arg(flags, "flags", _U8, R, dev), R, page_size,
+        _arg(free, "free", _I32, (num_pages + 31) // 32, dev), num_pages, _raw(stream, dev)), "engram_block_release")
 
 
 def engram_beam_select_workspace(G: int, K: int, V: int, n: int) -> int:
@@ -100,22 +109,25 @@ def engram_beam_select(logits, scores, tokens, parents, out_scores, *, workspace
     rows may be strided), scores float32 [G][K]; tokens, parents int32 [G][n] and out_scores
     float32 [G][n] are written, done_out uint8 [G][n] where given.  done uint8 [G][K] marks
     beams that have ended (end_token is then needed)."""
+    dev = _place(scores, "scores")
     _need(scores.dim() == 2 and tokens.dim() == 2, "scores must be [G][K], tokens [G][n]")
-    (G, K), n = scores.shape, tokens.shape[1]
+    (G, K), shape = scores.shape, tokens.shape
+    n = shape[1]
     lp, rows, V, ld, kind = _matrix(logits, "logits", _WIDE)
     _need(rows == G * K, "logits must have a row for every beam")
+    _need(logits.get_device() == dev, "logits are on another device")
+    if shape[0] != G or parents.shape != shape or out_scores.shape != shape:
+        raise ValueError("tokens, parents and out_scores must be [G][n]")
+    _need(done_out is None or done_out.shape == shape, "done_out must be [G][n]")
+    _need(done is None or done.shape == scores.shape, "done must be [G][K]")
     _need(-1 <= end_token < 1 << 31, "end_token must be a token or -1")
-    _count(G, "G"), _count(V, "V")
-    for t, name in ((tokens, "tokens"), (parents, "parents"), (out_scores, "out_scores"), (done_out, "done_out")):
-        _need(t is None or t.shape == (G, n), f"{name} must be [G][n]")
-    _need(done is None or done.shape == (G, K), "done must be [G][K]")
-    wp, wn = _work(workspace)
+    _count(rows, "G * K"), _count(V, "V")
     _check(_lib.engram_beam_select(
-        lp, kind, ld, G, K, V, _flat(scores, "scores", torch.float32), None if done is None else _flat(done, "done", _U8),
-        end_token, n, _flat(tokens, "tokens", _I32), _flat(parents, "parents", _I32),
-        _flat(out_scores, "out_scores", torch.float32), None if done_out is None else _flat(done_out, "done_out", _U8), wp, wn,
-        _serve_stream(stream, logits, scores, tokens, parents, out_scores, done, done_out, workspace)),
-        "engram_beam_select")
+        lp, kind, ld, G, K, V, _arg(scores, "scores", _F32, 0, dev), _arg(done, "done", _U8, 0, dev), end_token, n,
+        _arg(tokens, "tokens", _I32, 0, dev), _arg(parents, "parents", _I32, 0, dev),
+        _arg(out_scores, "out_scores", _F32, 0, dev), _arg(done_out, "done_out", _U8, 0, dev),
+        _arg(workspace, "workspace", workspace.dtype, 0, dev), workspace.numel() * workspace.element_size(),
+        _raw(stream, dev)), "engram_beam_select")
 
 
 def engram_beam_reorder(parents, *, slots=None, slots_out=None, store=None, slot_src=None, slot_dst=None, tables=None,
@@ -125,55 +137,51 @@ def engram_beam_reorder(parents, *, slots=None, slots_out=None, store=None, slot
     entries of ``store``, a Store, with them) and block tables int32 [G * K][blocks] with lens
     int32 [G * K] (into tables_out, or in place; pages that nothing names any more come back to
     free).  slot_src / slot_dst and page_src / page_dst int32 [G][K] receive the rows to copy."""
+    dev = _place(parents, "parents")
     _need(parents.dim() == 2, "parents must be [G][K]")
     G, K = parents.shape
     n = _count(G * K, "G * K")
-    if slots_out is None:
-        slots_out = slots
-    tp = op = None
+    tp = op = fp = None
     blocks = ld = 0
     if tables is not None:
-        tp, blocks, ld = _tables(tables, "tables", n)
-        op, out_blocks, out_ld = (tp, blocks, ld) if tables_out is None else _tables(tables_out, "tables_out", n)
+        tp, blocks, ld = _tables(tables, "tables", n, dev)
+        op, out_blocks, out_ld = (tp, blocks, ld) if tables_out is None else _tables(tables_out, "tables_out", n, dev)
         _need(out_blocks == blocks and (out_ld == ld or n <= 1), "tables_out must be laid out as tables")
         _need(lens is not None and page_size is not None and num_pages is not None,
               "tables need lens, page_size and num_pages")
         page_size, num_pages = _count(page_size, "page_size"), _count(num_pages, "num_pages")
+        fp = _arg(free, "free", _I32, (num_pages + 31) // 32, dev)
     else:
         _need(tables_out is None and free is None and page_src is None and page_dst is None, "pages need tables")
         page_size = num_pages = 0
+    sp = _arg(slots, "slots", _I32, n, dev)
     _check(_lib.engram_beam_reorder(
-        _of(parents, "parents", _I32, n), G, K, None if store is None else store.handle, _of(slots, "slots", _I32, n),
-        _of(slots_out, "slots_out", _I32, n), _of(slot_src, "slot_src", _I32, n), _of(slot_dst, "slot_dst", _I32, n), tp, op,
-        ld, blocks, _of(lens, "lens", _I32, n), page_size, None if free is None else _pool(free, "free", num_pages),
-        num_pages, _of(page_src, "page_src", _I32, n), _of(page_dst, "page_dst", _I32, n),
-        _serve_stream(stream, parents, slots, slots_out, slot_src, slot_dst, tables, tables_out, lens, free, page_src,
-                      page_dst)), "engram_beam_reorder")
+        _arg(parents, "parents", _I32, n, dev), G, K, None if store is None else store.handle, sp,
+        sp if slots_out is None else _arg(slots_out, "slots_out", _I32, n, dev), _arg(slot_src, "slot_src", _I32, n, dev),
+        _arg(slot_dst, "slot_dst", _I32, n, dev), tp, op, ld, blocks, _arg(lens, "lens", _I32, n, dev), page_size, fp,
+        num_pages, _arg(page_src, "page_src", _I32, n, dev), _arg(page_dst, "page_dst", _I32, n, dev), _raw(stream, dev)),
+        "engram_beam_reorder")
 
 
 def engram_state_copy(state, src, dst, *, stream=None):
     """Rows src -> dst (int32 [n], -1 for none) of state [rows][width] or, in every plane,
     [planes][rows][width]; any type, the last dimension contiguous."""
-    if not isinstance(state, torch.Tensor):
-        raise TypeError("state must be a tensor")
-    if not state.is_cuda:
-        raise TypeError("state must be a device tensor")
-    _need(state.dim() in (2, 3), "state must be [rows][width] or [planes][rows][width]")
-    rows, width = state.shape[-2:]
-    size = state.element_size()
-    strides = state.stride()
-    _need(width == 0 or strides[-1] == 1 or width == 1, "state must have contiguous rows")
+    dev = _place(state, "state")
+    shape, strides, size = state.shape, state.stride(), state.element_size()
+    _need(2 <= len(shape) <= 3, "state must be [rows][width] or [planes][rows][width]")
+    rows, width = shape[-2], shape[-1]
+    _need(width <= 1 or strides[-1] == 1, "state must have contiguous rows")
     pitch = width if rows <= 1 else strides[-2]
     _need(pitch >= width, "state must not have overlapping rows")
-    planes = state.shape[0] if state.dim() == 3 else 1
-    plane = strides[0] if planes > 1 else 0
-    _need(planes <= 1 or plane >= (rows - 1) * pitch + width or pitch >= (planes - 1) * plane + width > width,
-          "state must not have overlapping planes")
+    planes, plane = 1, 0
+    if len(shape) == 3 and shape[0] != 1:
+        planes, plane = shape[0], strides[0]
+        _need(planes == 0 or plane >= (rows - 1) * pitch + width or pitch >= (planes - 1) * plane + width > width,
+              "state must not have overlapping planes")
     n = _count(src.numel(), "n")
     _need(dst.numel() == n, "src and dst must be of one size")
-    sp, dp = _flat(src, "src", _I32), _flat(dst, "dst", _I32)
-    raw = _serve_stream(stream, state, src, dst)
+    sp, dp = _arg(src, "src", _I32, n, dev), _arg(dst, "dst", _I32, n, dev)
     if width == 0 or n == 0:
         return
-    _check(_lib.engram_state_copy(state.data_ptr(), planes, plane * size, rows, pitch * size, width * size, sp, dp, n, raw),
-           "engram_state_copy")
+    _check(_lib.engram_state_copy(state.data_ptr(), planes, plane * size, rows, pitch * size, width * size, sp, dp, n,
+                                  _raw(stream, dev)), "engram_state_copy")
