@@ -46,20 +46,65 @@ __device__ __forceinline__ unsigned long long select_key(float x, int token) {
 __device__ __forceinline__ float key_logit(unsigned long long key) { return from_order((uint32_t)(key >> 32)); }
 __device__ __forceinline__ int key_token(unsigned long long key) { return (int)~(uint32_t)key; }
 
-// The largest bound of `bits` leading bits that at least n lanes' values reach (n <= 64; 0 if
-// fewer than n lanes have any).
+// The largest bound of `bits` (even) leading bits that at least n lanes' values reach (n <= 64; 0
+// if fewer than n lanes have any): two bits a step, since every step waits for the last.
 __device__ __forceinline__ uint32_t bound_of_lanes(uint32_t value, int n, int bits) {
   uint32_t bound = 0;
-  for (int b = 31; b >= 32 - bits; --b) {
-    const uint32_t next = bound | 1u << b;
-    if (__popcll(__ballot(value >= next)) >= n) bound = next;
+  for (int b = 30; b >= 32 - bits; b -= 2) {
+    const uint32_t one = bound | 1u << b, two = bound | 2u << b, three = bound | 3u << b;
+    const int n1 = __popcll(__ballot(value >= one)), n2 = __popcll(__ballot(value >= two)),
+              n3 = __popcll(__ballot(value >= three));
+    bound = n3 >= n ? three : n2 >= n ? two : n1 >= n ? one : bound;
   }
   return bound;
 }
 
-// kVec logits from element e of a row on; those from V on are -inf.  A lane's elements go by
-// their place in the row, not by the row's place in its 16-byte lines (a load may start at any
-// element), so that equal rows have equal sums, and beams with equal totals keep their order.
+// Reductions over a wave by data-parallel moves (the last lane has the result, lanes without a
+// source take `none`), a third of the latency of six exchanges through LDS.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float moved(float none, float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(v), CTRL, ROWS, 0xf, false));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double none, double v) {
+  const int lo = __builtin_amdgcn_update_dpp(__double2loint(none), __double2loint(v), CTRL, ROWS, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(__double2hiint(none), __double2hiint(v), CTRL, ROWS, 0xf, false);
+  return __hiloint2double(hi, lo);
+}
+template <typename V, typename F>
+__device__ __forceinline__ V of_wave(V v, V none, F f) {
+  v = f(v, moved<0x111, 0xf>(none, v));  // row_shr 1, 2, 4, 8
+  v = f(v, moved<0x112, 0xf>(none, v));
+  v = f(v, moved<0x114, 0xf>(none, v));
+  v = f(v, moved<0x118, 0xf>(none, v));
+  v = f(v, moved<0x142, 0xa>(none, v));  // row_bcast 15, 31
+  return f(v, moved<0x143, 0xc>(none, v));
+}
+__device__ __forceinline__ float last_lane(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ double last_lane(double v) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), 63), __builtin_amdgcn_readlane(__double2loint(v), 63));
+}
+// (A NaN stays one.)
+__device__ __forceinline__ float max_of_wave(float v) {
+  return last_lane(of_wave(v, -INFINITY, [](float a, float b) { return __builtin_elementwise_maximum(a, b); }));
+}
+template <typename V>
+__device__ __forceinline__ V sum_of_wave(V v) {
+  return last_lane(of_wave(v, (V)0, [](V a, V b) { return a + b; }));
+}
+// Sum over groups of kRankLanes = 8 lanes, in all of them.
+__device__ __forceinline__ int sum_of_eight(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xf, 0xf, false);    // quad_perm 1, 0, 3, 2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xf, 0xf, false);    // quad_perm 2, 3, 0, 1
+  return v + __builtin_amdgcn_update_dpp(0, v, 0x141, 0xf, 0xf, false);  // row_half_mirror
+}
+
+// kVec logits from element e of a row on, or those below `end` and -inf for the others.  A lane's
+// elements go by their place in the row, not by the row's place in its 16-byte lines (a load may
+// start at any element), so that equal rows have equal sums, and beams with equal totals keep
+// their order.
 template <typename T>
 struct Logits;
 template <>
@@ -68,10 +113,12 @@ struct Logits<float> {
   typedef float raw_t __attribute__((ext_vector_type(4)));
   typedef raw_t anywhere_t __attribute__((aligned(4)));
   raw_t raw;
-  __device__ __forceinline__ void load(const float* x, int e) { raw = __builtin_nontemporal_load(reinterpret_cast<const anywhere_t*>(x + e)); }
-  __device__ __forceinline__ void load(const float* x, int e, int V) {
+  __device__ __forceinline__ void load(const float* x, int e) {
+    raw = __builtin_nontemporal_load(reinterpret_cast<const anywhere_t*>(x + e));
+  }
+  __device__ __forceinline__ void load_below(const float* x, int e, int end) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) raw[i] = e + i < V ? x[e + i] : -INFINITY;
+    for (int i = 0; i < kVec; ++i) raw[i] = e + i < end ? x[e + i] : -INFINITY;
   }
   __device__ __forceinline__ float at(int i) const { return raw[i]; }
   // at(i) for an i that is not known before, in LDS
@@ -84,12 +131,14 @@ struct Logits<uint16_t> {  // bf16
   typedef uint32_t raw_t __attribute__((ext_vector_type(4)));
   typedef raw_t anywhere_t __attribute__((aligned(2)));
   raw_t raw;
-  __device__ __forceinline__ void load(const uint16_t* x, int e) { raw = __builtin_nontemporal_load(reinterpret_cast<const anywhere_t*>(x + e)); }
-  __device__ __forceinline__ void load(const uint16_t* x, int e, int V) {
+  __device__ __forceinline__ void load(const uint16_t* x, int e) {
+    raw = __builtin_nontemporal_load(reinterpret_cast<const anywhere_t*>(x + e));
+  }
+  __device__ __forceinline__ void load_below(const uint16_t* x, int e, int end) {
 #pragma unroll
     for (int i = 0; i < kVec; i += 2) {
-      const uint32_t lo = e + i < V ? x[e + i] : 0xFF80u;
-      const uint32_t hi = e + i + 1 < V ? x[e + i + 1] : 0xFF80u;
+      const uint32_t lo = e + i < end ? x[e + i] : 0xFF80u;
+      const uint32_t hi = e + i + 1 < end ? x[e + i + 1] : 0xFF80u;
       raw[i / 2] = hi << 16 | lo;
     }
   }
@@ -133,20 +182,19 @@ __global__ __launch_bounds__(kSelectThreads, Logits<T>::kWaves) void beam_select
   __shared__ int loads, listed;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const T* x = static_cast<const T*>(a.logits) + row * a.ld;
-  const int first = piece * NV * kSelectThreads * kVec, end = min(a.V, first + NV * kSelectThreads * kVec);
-  const int e0 = first + tid * kVec;
+  constexpr int kBlock = kSelectThreads * kVec;
+  const int first = piece * NV * kBlock, end = min(a.V, first + NV * kBlock), e0 = first + tid * kVec;
   Logits<T> v[NV];
-  if (end - first == NV * kSelectThreads * kVec) {
+  if (end - first == NV * kBlock) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) v[j].load(x, e0 + j * kSelectThreads * kVec);
+    for (int j = 0; j < NV; ++j) v[j].load(x, e0 + j * kBlock);
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int e = e0 + j * kSelectThreads * kVec;
-      if (e + kVec <= end)
-        v[j].load(x, e);
+      if (e0 + j * kBlock + kVec <= end)
+        v[j].load(x, e0 + j * kBlock);
       else
-        v[j].load(x, e, end);
+        v[j].load_below(x, e0 + j * kBlock, end);
     }
   }
   if (tid == 0) loads = listed = 0;
@@ -167,9 +215,7 @@ __global__ __launch_bounds__(kSelectThreads, Logits<T>::kWaves) void beam_select
   const float of_lane = __builtin_elementwise_maximum(
       __builtin_elementwise_maximum(lane_max[0][lane], lane_max[1][lane]),
       __builtin_elementwise_maximum(lane_max[2][lane], lane_max[3][lane]));
-  float m = of_lane;
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) m = __builtin_elementwise_maximum(m, __shfl_xor(m, off, 64));
+  const float m = max_of_wave(of_lane);
   // the bound keeps 16 bits: exact for bf16, and 2^-8 below the n-th of the maxima for fp32
   const uint32_t reach = bound_of_lanes(in_order(of_lane), a.n, 16);
   const float bound = reach <= in_order(kLowest) ? kLowest : from_order(reach);
@@ -186,7 +232,7 @@ __global__ __launch_bounds__(kSelectThreads, Logits<T>::kWaves) void beam_select
       const int place = atomicAdd(&loads, 1);
       if (place < kSelectLoads) {
         load_list[place] = v[j];
-        load_at[place] = e0 + j * kSelectThreads * kVec;
+        load_at[place] = e0 + j * kBlock;
       }
     }
     if (!far) {
@@ -197,34 +243,38 @@ __global__ __launch_bounds__(kSelectThreads, Logits<T>::kWaves) void beam_select
       for (int i = 0; i < kVec; ++i) sum[i & 1] += v[j].at(i) == m ? 1.0f : 0.0f;
     }
   }
-  float s = sum[0] + sum[1];
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off, 64);
+  const float s = sum_of_wave(sum[0] + sum[1]);
   if (lane == 0) wave_sum[wave] = s;
   __syncthreads();
   if (tid == 0) a.parts[blockIdx.x] = make_float2(m, (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]));
-  const int held = min(loads, kSelectLoads) * kVec;
-  for (int i = tid; i < held; i += kSelectThreads) {
-    const float f = load_list[i / kVec].pick(i % kVec);
-    if (f >= bound) {
-      const int place = atomicAdd(&listed, 1);
-      if (place < kSelectList) list[place] = select_key(f, load_at[i / kVec] + i % kVec);
-    }
-  }
-  __syncthreads();
   unsigned long long* out = a.keys + (int64_t)blockIdx.x * a.n;
-  const int count = listed;
-  if (loads <= kSelectLoads && count <= kSelectList) {
-    for (int i = tid / kRankLanes; i < count; i += kSelectThreads / kRankLanes) {
-      const unsigned long long key = list[i];
-      int rank = 0;
-      for (int k = tid % kRankLanes; k < count; k += kRankLanes) rank += list[k] > key ? 1 : 0;
-#pragma unroll
-      for (int off = kRankLanes / 2; off >= 1; off >>= 1) rank += __shfl_xor(rank, off, 64);
-      if (rank < a.n && tid % kRankLanes == 0) out[rank] = key;
+  if (loads <= kSelectLoads) {
+    if (wave != 0 && loads <= kSelectList / kVec) return;  // one wave is enough, and the list cannot overflow
+    if (wave == 0) {
+      const int held = loads * kVec;
+      for (int i = lane; i < held; i += 64) {
+        const float f = load_list[i / kVec].pick(i % kVec);
+        if (f >= bound) {
+          const int place = atomicAdd(&listed, 1);
+          if (place < kSelectList) list[place] = select_key(f, load_at[i / kVec] + i % kVec);
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const int reached = listed;
+      if (reached <= kSelectList) {
+        for (int i = lane / kRankLanes; i < reached; i += 64 / kRankLanes) {
+          const unsigned long long key = list[i];
+          int rank = 0;
+          for (int k = lane % kRankLanes; k < reached; k += kRankLanes) rank += list[k] > key ? 1 : 0;
+          rank = sum_of_eight(rank);
+          if (rank < a.n && lane % kRankLanes == 0) out[rank] = key;
+        }
+        for (int i = reached + lane; i < a.n; i += 64) out[i] = 0;
+      }
     }
-    for (int i = count + tid; i < a.n; i += kSelectThreads) out[i] = 0;
-    return;
+    if (loads <= kSelectList / kVec) return;
+    __syncthreads();
+    if (listed <= kSelectList) return;
   }
   // too many equal ones: one by one from memory, each the largest key below the last
   __shared__ unsigned long long wave_best[4];
@@ -311,8 +361,7 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
     if (kind == 1) {
       float m = p.x;
       for (int i = lane + 64; i < S; i += 64) m = __builtin_elementwise_maximum(m, part[i].x);
-#pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) m = __builtin_elementwise_maximum(m, __shfl_xor(m, off, 64));
+      m = max_of_wave(m);
       kind = 0;
       if (isfinite(m)) {
         double z = 0.0;
@@ -323,8 +372,7 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
           const float scale = __builtin_amdgcn_exp2f((p.x - m) * kLog2e);
           z += (double)p.y * (double)scale * (1.0 + shift * 0.6931471805599453);
         }
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) z += __shfl_xor(z, off, 64);
+        z = sum_of_wave(z);
         most = (double)m;
         norm = log(z);
         if (isfinite(z)) kind = 1;
@@ -406,8 +454,7 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
       int rank = 0;
       for (int k = tid % kRankLanes; k < count; k += kRankLanes)
         rank += goes_before(totals[k], of_beam[k], keys[k], total, b, key) ? 1 : 0;
-#pragma unroll
-      for (int off = kRankLanes / 2; off >= 1; off >>= 1) rank += __shfl_xor(rank, off, 64);
+      rank = sum_of_eight(rank);
       if (rank < n && tid % kRankLanes == 0) write(rank, total, b, key);
     }
     for (int r = count + tid; r < n; r += THREADS) write_none(r);
@@ -476,7 +523,7 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
 }
 
 // ---------------------------------------------------------------------------
-// Pieces of a row of V elements.
+// Pieces of a row of V elements, of up to nv blocks each.
 static int select_splits(int V, int vec, int nv) {
   const int per = nv * vec * kSelectThreads;
   return (V + per - 1) / per;
