@@ -741,4 +741,5 @@ from .serve_ops import (  # noqa: E402  (needs the functions above)
     engram_beam_reorder, engram_beam_select, engram_beam_select_workspace, engram_block_plan, engram_block_release,
     engram_state_copy)
 from .runtime import Engram, pad_weight  # noqa: E402  (needs the functions above)
+from .serving import BeamDecode  # noqa: E402
 from .training import SiteTraining  # noqa: E402
