@@ -81,6 +81,9 @@ class BeamDecode:
         self._work = torch.empty(max(engram_beam_select_workspace(G, 1, vocab, K),
                                      engram_beam_select_workspace(G, K, vocab, K)), dtype=torch.uint8, device="cuda")
         self._all = torch.ones(n, dtype=torch.uint8, device="cuda")
+        self._none = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        self._each = torch.arange(n + 1, **i32)
+        self._started = False
         self._rows_planned(0, 0)
 
     def _rows_planned(self, rows, tokens):
@@ -94,10 +97,13 @@ class BeamDecode:
         token_slots, positions and seq_start are those of the prompts."""
         import torch
         G, K, P = self.requests, self.beams, self.page_size
+        if self._started:
+            raise RuntimeError("the last prompts' beams still hold their pages: call finish first")
         if tuple(lens.shape) != (G,) or lens.dtype != torch.int32:
             raise ValueError("lens must be int32 [requests]")
         if not 0 <= num_tokens <= self.max_prompt_tokens:
             raise ValueError(f"{num_tokens} tokens, max_prompt_tokens is {self.max_prompt_tokens}")
+        self._started = True
         pool = dict(page_size=P, num_pages=self.num_pages, stream=stream)
         with _on(stream):
             past, new = self._past[:G * K].view(G, K), self._new[:G * K].view(G, K)
@@ -142,14 +148,17 @@ class BeamDecode:
                           positions=self.positions, seq_start=self.seq_start, lens=self.lens, stream=stream)
 
     def step(self, streams, *, stream=None):
-        """The n-gram memory of the selected tokens added into streams [requests * beams][hc][hidden].
-        A beam without a token (none was left to select) counts as dead."""
+        """The n-gram memory of the selected tokens added into streams [requests * beams][hc][hidden]
+        (several sites: one such tensor each).  A beam without a token (none was left to select)
+        counts as dead."""
         import torch
         with _on(stream):
             flat = self.tokens.view(-1)
             dead, keep = (flat < 0).to(torch.uint8), (flat >= 0).to(torch.uint8)
-        return self.engram.decode_step(flat, streams, slots=self.slots.view(-1), store=self.store, dead=dead, keep=keep,
-                                       stream=stream)
+        args = dict(slots=self.slots.view(-1), store=self.store, dead=dead, keep=keep, stream=stream)
+        if self.engram.decode_lookup_supported:
+            return self.engram.decode_step(flat, streams, **args)
+        return self.engram.forward(flat, self._each, streams, seq_start=self._none, **args)
 
     def select(self, logits, *, stream=None):
         """The next tokens from logits [requests * beams][vocab] of the last ones; slots, store,
@@ -172,6 +181,7 @@ class BeamDecode:
                              num_pages=self.num_pages, stream=stream)
         with _on(stream):
             self.lens.zero_()
+        self._started = False
 
 
 def _on(stream):

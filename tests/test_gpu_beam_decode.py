@@ -115,15 +115,17 @@ def test_search_with_paged_caches(G, K, P, V, steps, end):
         search = HostSearch(prompts, K, end)
 
 
-def test_search_with_the_memory_of_a_site():
+@pytest.mark.parametrize("table_dtype", ["fp8", "bf16"])
+def test_search_with_the_memory_of_a_site(table_dtype):
     """Prefill, selection and single steps of a site: the store's slots and the looked-up rows are
-    those of every beam's whole sequence."""
-    cfg = ei.get_config("decode_tiny")
+    those of every beam's whole sequence.  (bf16 tables have no lookup in one launch.)"""
+    cfg = ei.get_config("decode_tiny", table_dtype=table_dtype)
     rng = np.random.default_rng(11)
     G, K, P, V, steps = 5, 4, 4, cfg.vocab, 9
     lens = rng.integers(1, 12, G)
     prompts = [rng.integers(0, V, n).tolist() for n in lens]
     site = Site(cfg, max_tokens=int(lens.sum()) + G * K).site
+    assert site.decode_lookup_supported == (table_dtype == "fp8")
     check = Site(cfg, max_tokens=2048).site
     d = eng.BeamDecode(site, requests=G, beams=K, max_len=64, page_size=P, vocab=V)
     search = HostSearch(prompts, K, -1)
@@ -227,6 +229,12 @@ def test_construction_refuses():
     for lens, n in ((dev([1]), 2), (dev([1, 1], torch.int64), 2), (dev([1, 1]), 17), (dev([1, 1]), -1)):
         with pytest.raises(ValueError):
             d.start(lens, n)
+    d.start(dev([1, 1]), 2)
+    with pytest.raises(RuntimeError):
+        d.start(dev([1, 1]), 2)
+    d.finish()
+    d.start(dev([1, 1]), 2)
+    assert eng.engram_get_error() == 0
 
 
 # ---------------------------------------------------------------------------

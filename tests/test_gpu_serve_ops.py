@@ -396,6 +396,24 @@ def test_select_equal_logits(V, n, dtype):
     assert tokens[0][:len(first)].tolist() == first and (parents[0][:len(first)] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("G, K, V, n", [(1, 64, 5000, 64), (300, 1, 32_768, 3), (1, 64, 64, 64)])
+def test_select_equal_logits_past_every_list(G, K, V, n, dtype):
+    """More equal candidates than the lists of a piece, of its loads and of a request hold."""
+    x = np.zeros((G * K, V))
+    scores = np.zeros((G, K), dtype=np.float32)
+    tokens, parents, *_ = check_select(x, scores, None, -1, n, dtype)
+    assert (tokens == np.arange(n)).all() and (parents == 0).all()
+    scores[:, ::2] = -1.0
+    done = np.zeros((G, K), dtype=np.uint8)
+    done[:, -1] = 1  # an ended beam's one candidate, the best of all
+    scores[:, -1] = 1.0
+    if K > 1:
+        tokens, parents, *_ = check_select(x, scores, done, V - 1, n, dtype)
+        assert (tokens[:, 0] == V - 1).all() and (parents[:, 0] == K - 1).all()
+        assert (tokens[:, 1:] == np.arange(n - 1)).all() and (parents[:, 1:] == 1).all()
+
+
 def test_select_zeros_of_both_signs_are_equal():
     x = np.zeros((1, 600))
     x[0, ::2] = -0.0
