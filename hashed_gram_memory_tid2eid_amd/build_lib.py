@@ -3,7 +3,9 @@
 Usage: ``python hashed_gram_memory_tid2eid_amd/build_lib.py`` (run by path: importing
 the package loads the library this script builds).  Compiles the single
 device translation unit and the host sources to objects under ``_build/`` and
-links ``hashed_gram_memory_tid2eid_amd/libengram.so``.  Always recompiles.
+links ``hashed_gram_memory_tid2eid_amd/libengram.so``; beside it the Python binding's
+extension module ``_tensor_args.so`` with g++ against the installed torch.  Always
+recompiles.
 
 The library carries a hash of what it was built from (every source under
 ``csrc/`` and ``include/`` plus the compiler flags), readable with
@@ -23,6 +25,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libengram.so")
+TENSOR_ARGS = os.path.join(PKG, "_tensor_args.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -69,10 +72,24 @@ def built_hash(lib: str = LIB):
     return m.group(1).decode() if m else None
 
 
+def tensor_args_command(out: str):
+    """How _tensor_args.so is built: the torch libraries it names are those that `import torch`
+    has loaded by the time it is imported."""
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    includes = [x for path in cpp_extension.include_paths() for x in ("-isystem", path)]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *includes,
+            "-I", sysconfig.get_paths()["include"], f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            os.path.join(CSRC, "tensor_args.cpp"), "-o", out, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     sha = source_hash()
-    procs = []
+    cmd = tensor_args_command(TENSOR_ARGS + ".tmp")
+    procs = [("tensor_args.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT))]
     objs = []
     for src in SOURCES:
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
@@ -99,6 +116,7 @@ def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     subprocess.run(cmd, check=True)
+    os.replace(TENSOR_ARGS + ".tmp", TENSOR_ARGS)
     os.replace(tmp, LIB)
     return LIB
 
@@ -139,7 +157,7 @@ def ensure_built() -> str:
     """Builds the library when it is missing or was built from other sources than
     the tree holds now (compared by the embedded source hash); otherwise leaves
     the built one in place."""
-    if built_hash() == source_hash():
+    if built_hash() == source_hash() and os.path.exists(TENSOR_ARGS):
         return LIB
     return build()
 

@@ -12,53 +12,35 @@ import ctypes
 
 import torch
 
-from . import _check, _dev, _lib, _need, _stream
-from .train_ops import _INT, _WIDE, _matrix
+from . import ENGRAM_DTYPE_BF16, ENGRAM_DTYPE_F32, _check, _lib, _need, _stream
+
+try:
+    from ._tensor_args import address as _arg, device as _place, matrix as _rows
+except ImportError as e:
+    raise ImportError("_tensor_args.so is missing or does not fit this torch: build it with "
+                      "`python hashed_gram_memory_tid2eid_amd/build_lib.py`") from e
 
 _I32, _I64, _U8, _F32 = torch.int32, torch.int64, torch.uint8, torch.float32
-
-
-def _place(t, name):
-    """The device of a call, which is that of its tensors and the current one."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a device tensor")
-    dev = t.get_device()
-    if dev != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on device {dev}, the current device is {torch._C._cuda_getDevice()}")
-    return dev
+_LOGITS = {torch.bfloat16: ENGRAM_DTYPE_BF16, torch.float32: ENGRAM_DTYPE_F32}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _raw(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-
-
-def _arg(t, name, dtype, least, dev):
-    """Pointer of a contiguous tensor of at least so many elements on the call's device, or None."""
-    if t is None:
-        return None
-    try:
-        if t.dtype is dtype and t.get_device() == dev and t.numel() >= least and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _dev(t, dtype, name)  # says what is wrong, if it is one of these
-    _need(t.numel() >= least, f"{name} too small")
-    raise ValueError(f"{name} is on device {t.get_device()}, the call on device {dev}")
+    return _raw_stream(dev) if stream is None else _stream(stream)
 
 
 def _count(n, name):
     """A whole number that a 32-bit argument holds."""
-    n = int(n)
-    if not 0 <= n < 1 << 31:
-        raise ValueError(f"{name} must be in [0, 2^31), got {n}")
-    return n
+    if not 0 <= n < 1 << 31 or n != int(n):
+        raise ValueError(f"{name} must be a whole number in [0, 2^31), got {n}")
+    return int(n)
 
 
 def _tables(t, name, rows, dev):
     """(pointer, columns, leading dimension) of a table of so many rows."""
-    p, n, blocks, ld, _ = _matrix(t, name, _INT)
-    _need(n == rows, f"{name} must have {rows} rows")
-    _need(t.get_device() == dev, f"{name} is on another device")
+    p, n, blocks, ld = _rows(t, name, _I32, dev)
+    if n != rows:
+        raise ValueError(f"{name} must have {rows} rows, got {n}")
     return p, blocks, ld
 
 
@@ -113,9 +95,11 @@ def engram_beam_select(logits, scores, tokens, parents, out_scores, *, workspace
     _need(scores.dim() == 2 and tokens.dim() == 2, "scores must be [G][K], tokens [G][n]")
     (G, K), shape = scores.shape, tokens.shape
     n = shape[1]
-    lp, rows, V, ld, kind = _matrix(logits, "logits", _WIDE)
+    lp, rows, V, ld = _rows(logits, "logits", None, dev)
+    kind = _LOGITS.get(logits.dtype)
+    if kind is None:
+        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
     _need(rows == G * K, "logits must have a row for every beam")
-    _need(logits.get_device() == dev, "logits are on another device")
     if shape[0] != G or parents.shape != shape or out_scores.shape != shape:
         raise ValueError("tokens, parents and out_scores must be [G][n]")
     _need(done_out is None or done_out.shape == shape, "done_out must be [G][n]")

@@ -663,3 +663,69 @@ def test_copy_passes_32_bits():
     eng.engram_state_copy(state, dev([7]), dev([(1 << 20) - 1]))
     assert status() == 0
     assert (state[:, -1] == 3).all() and int(state[:, -2].sum()) == 0 and int(state[4, 0].sum()) == 0
+
+
+# ---------------------------------------------------------------------------
+# the binding's refusals of device tensors
+# ---------------------------------------------------------------------------
+
+def zeros(*shape, dtype=I32):
+    return torch.zeros(shape, dtype=dtype, device="cuda")
+
+
+def refused(fn, good, changes):
+    fn(**good())
+    torch.cuda.synchronize()
+    for change in changes:
+        with pytest.raises((TypeError, ValueError)):
+            fn(**dict(good(), **change))
+    assert status() == 0
+
+
+def test_binding_refuses_wrong_device_tensors():
+    def plan():
+        return dict(past=zeros(3), new=zeros(3), tables=zeros(3, 4), free=zeros(2), page_size=4, num_pages=64,
+                    cu_seqlens=zeros(4), token_slots=zeros(5, dtype=I64), positions=zeros(5), lens=zeros(3),
+                    seq_start=zeros(3, dtype=U8), free_out=zeros(2))
+    refused(eng.engram_block_plan, plan, [
+        dict(past=zeros(3, dtype=I64)), dict(past=zeros(6)[::2]), dict(new=zeros(2)), dict(new=zeros(3).cpu()),
+        dict(tables=zeros(2, 4)), dict(tables=zeros(4, 3).t()), dict(tables=zeros(1, 4).expand(3, 4)), dict(tables=zeros(12)),
+        dict(free=zeros(1)), dict(free=None, num_pages=1 << 31), dict(free_out=zeros(1)), dict(cu_seqlens=zeros(3)),
+        dict(token_slots=zeros(5)), dict(positions=zeros(4)), dict(lens=zeros(2)), dict(seq_start=zeros(3)),
+        dict(num_pages=-1), dict(page_size=1 << 33), dict(page_size=1.5), dict(past=None), dict(past=[1, 2, 3])])
+
+    def release():
+        return dict(tables=zeros(3, 4), lens=zeros(3), flags=zeros(3, dtype=U8), free=zeros(2), page_size=4, num_pages=64)
+    refused(eng.engram_block_release, release, [
+        dict(tables=zeros(4, 4)), dict(lens=zeros(2)), dict(flags=zeros(3)), dict(flags=zeros(2, dtype=U8)), dict(free=zeros(1)),
+        dict(num_pages=1 << 40)])
+
+    def select():
+        work = eng.engram_beam_select_workspace(2, 3, 50, 4)
+        return dict(logits=zeros(6, 50, dtype=torch.float32), scores=zeros(2, 3, dtype=torch.float32), tokens=zeros(2, 4),
+                    parents=zeros(2, 4), out_scores=zeros(2, 4, dtype=torch.float32), done=zeros(2, 3, dtype=U8), end_token=1,
+                    done_out=zeros(2, 4, dtype=U8), workspace=zeros(work, dtype=U8))
+    refused(eng.engram_beam_select, select, [
+        dict(logits=zeros(6, 50, dtype=torch.float16)), dict(logits=zeros(5, 50, dtype=torch.float32)),
+        dict(logits=zeros(1, 50, dtype=torch.float32).expand(6, 50)), dict(logits=zeros(50, 6, dtype=torch.float32).t()),
+        dict(logits=zeros(2, 3, 50, dtype=torch.float32)), dict(scores=zeros(6, dtype=torch.float32)), dict(scores=zeros(2, 3)),
+        dict(tokens=zeros(2, 4, dtype=I64)), dict(parents=zeros(2, 3)), dict(out_scores=zeros(2, 4)), dict(tokens=zeros(1, 4)),
+        dict(done=zeros(2, 4, dtype=U8)), dict(done_out=zeros(2, 3, dtype=U8)), dict(end_token=1 << 31), dict(end_token=-2),
+        dict(scores=zeros(2, 6, dtype=torch.float32)[:, ::2])])
+    with pytest.raises(eng.EngramError):
+        eng.engram_beam_select(**dict(select(), workspace=zeros(8, dtype=U8)))
+
+    def reorder():
+        return dict(parents=zeros(2, 3), slots=zeros(2, 3), slot_src=zeros(2, 3), slot_dst=zeros(2, 3), tables=zeros(6, 4),
+                    tables_out=zeros(6, 4), lens=zeros(6), page_size=4, num_pages=64, free=zeros(2), page_src=zeros(2, 3),
+                    page_dst=zeros(2, 3))
+    refused(eng.engram_beam_reorder, reorder, [
+        dict(parents=zeros(6)), dict(slots=zeros(5)), dict(slot_src=zeros(2, 3, dtype=I64)), dict(tables=zeros(5, 4)),
+        dict(tables_out=zeros(6, 5)), dict(tables_out=zeros(6, 8)[:, :4]), dict(lens=None), dict(page_size=None),
+        dict(num_pages=None), dict(free=zeros(1)), dict(page_dst=zeros(5)), dict(tables=None), dict(lens=zeros(5))])
+
+    def copy():
+        return dict(state=zeros(4, 5), src=zeros(2) - 1, dst=zeros(2) - 1)
+    refused(eng.engram_state_copy, copy, [
+        dict(state=zeros(5)), dict(state=zeros(2, 2, 2, 2)), dict(state=zeros(5, 4).t()), dict(state=zeros(1, 5).expand(4, 5)),
+        dict(src=zeros(3)), dict(dst=zeros(2, dtype=I64)), dict(src=zeros(2).cpu()), dict(state=zeros(4, 5).cpu())])

@@ -134,3 +134,23 @@ def test_binding_refuses_what_is_not_a_device_tensor():
         eng.engram_state_copy(i32(4, 4), i32(2), i32(2))
     with pytest.raises((TypeError, ValueError)):
         eng.engram_beam_select(torch.zeros(4, 10), torch.zeros(2, 2), i32(2, 2), i32(2, 2), torch.zeros(2, 2), workspace=i32(64))
+
+
+def test_tensor_arguments_of_the_wrong_kind():
+    from hashed_gram_memory_tid2eid_amd import _tensor_args as ta
+    host = torch.zeros(4, dtype=torch.int32)
+    assert ta.address(None, "x", torch.int32, 4, 0) is None
+    for call in (lambda t: ta.device(t, "x"), lambda t: ta.address(t, "x", torch.int32, 1, 0),
+                 lambda t: ta.matrix(t, "x", torch.int32, 0)):
+        for wrong in (host, [1, 2], 7, "x"):
+            with pytest.raises(TypeError):
+                call(wrong)
+    for args in ((), (host,), (host, "x", torch.int32, 1, 0, 0)):
+        with pytest.raises(TypeError):
+            ta.address(*args)
+    with pytest.raises(TypeError):
+        ta.device(host, 3)
+    for bad in (-1, 1 << 31, 1.5):
+        with pytest.raises(ValueError):
+            eng.serve_ops._count(bad, "x")
+    assert eng.serve_ops._count(7, "x") == 7
