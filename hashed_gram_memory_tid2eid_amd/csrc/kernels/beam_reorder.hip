@@ -156,9 +156,10 @@ hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t stream) {
 
 // ---------------------------------------------------------------------------
 // Rows copied as named: 4 units (of 16, 4 or 1 bytes) a lane, as many lanes a row as its length
-// takes, up to a workgroup, which then takes one piece of it.  Stores go past the caches (256
-// pairs of 16 KB in 32 planes, 268 MB: 40 us, 6.7 TB/s; ordinary stores 52; loads past them, too,
-// 56; 8 units a lane, ordinary stores, 110).
+// takes, up to a workgroup, which then takes one piece of it; a pair's planes by neighbouring
+// workgroups.  Bound by memory: 256 pairs of 16 KB in 32 planes, 268 MB, 51 us (5.3 TB/s).  Plane
+// by plane 55; ordinary stores 60; loads past the caches, too, 54; one unit a lane 62; 2,048
+// workgroups that go on from item to item 62.
 
 constexpr int kCopyThreads = 256;
 typedef uint32_t copy16_t __attribute__((ext_vector_type(4)));
@@ -170,7 +171,7 @@ __global__ __launch_bounds__(kCopyThreads) void state_copy_kernel(StateCopyArgs 
   const uint64_t item = (uint64_t)blockIdx.x * per + threadIdx.x / lanes;
   const uint64_t items = (uint64_t)a.n * (uint64_t)a.planes;
   if (item >= items) return;
-  const int64_t plane = (int64_t)(item / (uint32_t)a.n), pair = (int64_t)(item % (uint32_t)a.n);
+  const int64_t pair = (int64_t)(item / (uint32_t)a.planes), plane = (int64_t)(item % (uint32_t)a.planes);
   const int32_t src = a.src[pair], dst = a.dst[pair];
   if (src == -1 || dst == -1 || src == dst) return;
   if (src < 0 || dst < 0 || src >= a.rows || dst >= a.rows) {

@@ -21,7 +21,12 @@ namespace engram {
 constexpr int kSelectThreads = 256;
 constexpr int kSelectHeld = 4096;  // elements of the loads that hold one which reaches the bound
 constexpr int kSelectList = 1024;  // elements that reach it
+constexpr int kFewLoads = 16;      // loads that one wave ranks; their elements cannot overflow the list
 constexpr int kRankLanes = 8;      // lanes that count the larger ones of one element together
+// Up to so many of 64 values the n-th largest is a good bound: some 45 elements reach it where n
+// is 32.  All 64 are reached by hundreds, so more of them take 256 values (64 candidates of 64 x
+// 16 rows of 65,536 bf16: 778 us by 64, most of them one by one because the lists overflow).
+constexpr int kFewCandidates = 32;
 constexpr int kMergeList = 2048;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.44269504088896341f;
@@ -55,6 +60,18 @@ __device__ __forceinline__ uint32_t bound_of_lanes(uint32_t value, int n, int bi
     const int n1 = __popcll(__ballot(value >= one)), n2 = __popcll(__ballot(value >= two)),
               n3 = __popcll(__ballot(value >= three));
     bound = n3 >= n ? three : n2 >= n ? two : n1 >= n ? one : bound;
+  }
+  return bound;
+}
+
+// The same for 256 values, four of them a lane.
+__device__ __forceinline__ uint32_t bound_of_four(uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3, int n, int bits) {
+  uint32_t bound = 0;
+  for (int b = 31; b >= 32 - bits; --b) {
+    const uint32_t next = bound | 1u << b;
+    const int count = __popcll(__ballot(v0 >= next)) + __popcll(__ballot(v1 >= next)) + __popcll(__ballot(v2 >= next)) +
+                      __popcll(__ballot(v3 >= next));
+    if (count >= n) bound = next;
   }
   return bound;
 }
@@ -212,12 +229,13 @@ __global__ __launch_bounds__(kSelectThreads, Logits<T>::kWaves) void beam_select
   }
   lane_max[wave][lane] = mine;
   __syncthreads();
-  const float of_lane = __builtin_elementwise_maximum(
-      __builtin_elementwise_maximum(lane_max[0][lane], lane_max[1][lane]),
-      __builtin_elementwise_maximum(lane_max[2][lane], lane_max[3][lane]));
+  const float m0 = lane_max[0][lane], m1 = lane_max[1][lane], m2 = lane_max[2][lane], m3 = lane_max[3][lane];
+  const float of_lane = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m0, m1), __builtin_elementwise_maximum(m2, m3));
   const float m = max_of_wave(of_lane);
   // the bound keeps 16 bits: exact for bf16, and 2^-8 below the n-th of the maxima for fp32
-  const uint32_t reach = bound_of_lanes(in_order(of_lane), a.n, 16);
+  const uint32_t reach = a.n <= kFewCandidates
+                             ? bound_of_lanes(in_order(of_lane), a.n, 16)
+                             : bound_of_four(in_order(m0), in_order(m1), in_order(m2), in_order(m3), a.n, 16);
   const float bound = reach <= in_order(kLowest) ? kLowest : from_order(reach);
 
   // exp(x - m) as 2^(x log2e - c), c the float next to m log2e: one fma, rounded by 2^-24 of the
@@ -249,32 +267,32 @@ __global__ __launch_bounds__(kSelectThreads, Logits<T>::kWaves) void beam_select
   if (tid == 0) a.parts[blockIdx.x] = make_float2(m, (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]));
   unsigned long long* out = a.keys + (int64_t)blockIdx.x * a.n;
   if (loads <= kSelectLoads) {
-    if (wave != 0 && loads <= kSelectList / kVec) return;  // one wave is enough, and the list cannot overflow
-    if (wave == 0) {
-      const int held = loads * kVec;
-      for (int i = lane; i < held; i += 64) {
-        const float f = load_list[i / kVec].pick(i % kVec);
-        if (f >= bound) {
-          const int place = atomicAdd(&listed, 1);
-          if (place < kSelectList) list[place] = select_key(f, load_at[i / kVec] + i % kVec);
-        }
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      const int reached = listed;
-      if (reached <= kSelectList) {
-        for (int i = lane / kRankLanes; i < reached; i += 64 / kRankLanes) {
-          const unsigned long long key = list[i];
-          int rank = 0;
-          for (int k = lane % kRankLanes; k < reached; k += kRankLanes) rank += list[k] > key ? 1 : 0;
-          rank = sum_of_eight(rank);
-          if (rank < a.n && lane % kRankLanes == 0) out[rank] = key;
-        }
-        for (int i = reached + lane; i < a.n; i += 64) out[i] = 0;
+    // one wave is enough for few of them, and needs no barriers
+    const int workers = loads <= kFewLoads ? 64 : kSelectThreads;
+    if (tid >= workers) return;
+    for (int i = tid; i < loads * kVec; i += workers) {
+      const float f = load_list[i / kVec].pick(i % kVec);
+      if (f >= bound) {
+        const int place = atomicAdd(&listed, 1);
+        if (place < kSelectList) list[place] = select_key(f, load_at[i / kVec] + i % kVec);
       }
     }
-    if (loads <= kSelectList / kVec) return;
-    __syncthreads();
-    if (listed <= kSelectList) return;
+    if (workers == 64)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    else
+      __syncthreads();
+    const int reached = listed;
+    if (reached <= kSelectList) {
+      for (int i = tid / kRankLanes; i < reached; i += workers / kRankLanes) {
+        const unsigned long long key = list[i];
+        int rank = 0;
+        for (int k = tid % kRankLanes; k < reached; k += kRankLanes) rank += list[k] > key ? 1 : 0;
+        rank = sum_of_eight(rank);
+        if (rank < a.n && tid % kRankLanes == 0) out[rank] = key;
+      }
+      for (int i = reached + tid; i < a.n; i += workers) out[i] = 0;
+      return;
+    }
   }
   // too many equal ones: one by one from memory, each the largest key below the last
   __shared__ unsigned long long wave_best[4];
@@ -322,25 +340,25 @@ constexpr int kMergeKeys = 8;
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a) {
   __shared__ MergeBeams beams;
-  __shared__ uint32_t lane_max[THREADS];
+  __shared__ uint32_t slot_max[256];
   __shared__ double totals[kMergeList];
   __shared__ unsigned long long keys[kMergeList];
   __shared__ uint8_t of_beam[kMergeList];
   __shared__ int listed;
   const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int S = a.splits, K = a.K, n = a.n;
-  // place i of the request's keys is the (i / pieces)-th of piece i % pieces, so that the lanes
-  // share the pieces' first keys evenly
+  // place i of the request's keys is the (i / pieces)-th of piece i % pieces: the largest first
   const int pieces = K * S, places = pieces * n;
   const unsigned long long* all = a.keys + (int64_t)g * places;
   unsigned long long mine[kMergeKeys];  // (of beams that are not live: not written, and not looked at)
-  int piece_of[kMergeKeys];
+  int piece_of[kMergeKeys], slot_of[kMergeKeys];
   {
     int piece = tid % pieces, order = tid / pieces;
     const int step = THREADS % pieces, steps = THREADS / pieces;
 #pragma unroll
     for (int q = 0; q < kMergeKeys; ++q) {
       piece_of[q] = piece;
+      slot_of[q] = (piece + 13 * order) & 255;
       mine[q] = order < n ? all[piece * n + order] : 0;
       piece += step;
       order += steps;
@@ -351,6 +369,7 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
     }
   }
   if (tid == 0) listed = 0;
+  if (tid < 256) slot_max[tid] = 0;
   for (int b = wave; b < K; b += THREADS / 64) {
     const int row = g * K + b;
     const float2* part = a.parts + (int64_t)row * S;
@@ -387,9 +406,10 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
   }
   __syncthreads();
 
-  // a bound that n of 64 lanes reach, by the 12 leading bits of the totals' mantissas
+  // A bound that n of 64 (or 256) slots reach, by the 12 leading bits of the totals' mantissas.
+  // Every key counts for a slot by its piece and its rank there, so that the slots have equal
+  // shares of the best keys even where one beam has them all.
   double total[kMergeKeys];
-  uint32_t top = 0;
 #pragma unroll
   for (int q = 0; q < kMergeKeys; ++q) {
     if (mine[q] == 0) continue;
@@ -399,14 +419,12 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
       continue;
     }
     total[q] = beam_total(beams, piece_of[q], mine[q]);
-    top = max(top, high_in_order(total[q]));
+    atomicMax(&slot_max[slot_of[q]], high_in_order(total[q]));
   }
-  lane_max[tid] = top;
   __syncthreads();
-  uint32_t of_lane = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 64; ++w) of_lane = max(of_lane, lane_max[w * 64 + lane]);
-  const uint32_t bound = bound_of_lanes(of_lane, n, 24);
+  const uint32_t s0 = slot_max[lane], s1 = slot_max[64 + lane], s2 = slot_max[128 + lane], s3 = slot_max[192 + lane];
+  const uint32_t bound = n <= kFewCandidates ? bound_of_lanes(max(max(s0, s1), max(s2, s3)), n, 24)
+                                             : bound_of_four(s0, s1, s2, s3, n, 24);
 
   auto push = [&](double total, int b, unsigned long long key) {
     const int place = atomicAdd(&listed, 1);
@@ -419,13 +437,20 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
 #pragma unroll
   for (int q = 0; q < kMergeKeys; ++q)
     if (mine[q] != 0 && high_in_order(total[q]) >= bound) push(total[q], piece_of[q], mine[q]);
-  for (int i = tid + kMergeKeys * THREADS; i < places; i += THREADS) {
-    const int piece = i % pieces, b = piece / S;
-    if (beams.kind[b] != 1) continue;
-    const unsigned long long key = all[piece * n + i / pieces];
-    if (key == 0) continue;
-    const double t = beam_total(beams, b, key);
-    if (high_in_order(t) >= bound) push(t, b, key);
+  // the keys that no thread has: a piece's descend, so it is left at the first below the bound
+  if (places > kMergeKeys * THREADS) {
+    for (int piece = tid; piece < pieces; piece += THREADS) {
+      const int b = piece / S;
+      if (beams.kind[b] != 1) continue;
+      const int known = piece < kMergeKeys * THREADS ? (kMergeKeys * THREADS - piece + pieces - 1) / pieces : 0;
+      for (int order = known; order < n; ++order) {
+        const unsigned long long key = all[(int64_t)piece * n + order];
+        if (key == 0) break;
+        const double t = beam_total(beams, b, key);
+        if (high_in_order(t) < bound) break;
+        push(t, b, key);
+      }
+    }
   }
   if (tid < K && beams.kind[tid] == 2) push(beams.score[tid], tid, select_key(0.0f, a.end_token));
   __syncthreads();
@@ -529,12 +554,12 @@ static int select_splits(int V, int vec, int nv) {
   return (V + per - 1) / per;
 }
 
-// Loads a lane: as many as leave this many workgroups, up to 8.
+// Loads a lane: as many as leave this many workgroups, up to 8 and to what a row takes.
 constexpr int kSelectGroups = 1024;
 
 static int select_loads(int64_t rows, int V, int vec) {
   int nv = 8;
-  while (nv > 1 && rows * select_splits(V, vec, nv) < kSelectGroups) nv >>= 1;
+  while (nv > 1 && (rows * select_splits(V, vec, nv) < kSelectGroups || select_splits(V, vec, nv / 2) == 1)) nv >>= 1;
   return nv;
 }
 
