@@ -15,6 +15,9 @@ namespace engram {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWords = 8;                           // words of the bitmap a thread loads at a time
+// Up to so many pages are looked for one by one (4,096 of 64 rows 20 us, 8,192 32, 65,536 219),
+// more are handed out by the threads in whose words they are (28, 29, 50).
+constexpr uint32_t kPlanSearched = 6144;
 constexpr uint32_t kSat = 0x7FFFFFFFu;                  // sums stop here instead of wrapping round
 
 __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) {
@@ -276,11 +279,36 @@ __global__ __launch_bounds__(kPlanThreads) void block_plan_kernel(PlanArgs a) {
       page[0] = find_page(a, sums, TILES * kPlanThreads, stretch, words, before[ROWS]);
       a.tables[tid * a.table_ld + block_at(a, p[0])] = page[0];
     }
-  } else {
+  } else if (num_new <= kPlanSearched) {
     for (uint32_t k = tid; k < num_new; k += kPlanThreads) {
       const int row = last_at_most(first, a.R, k);
       a.tables[row * a.table_ld + blocks_in(a, past[row]) + (k - first[row])] =
           find_page(a, sums, TILES * kPlanThreads, stretch, words, k);
+    }
+  } else {
+    // every thread hands out the pages of its own words, in order, and goes along the rows
+#pragma unroll 1
+    for (int j = 0; j < TILES; ++j) {
+      const int64_t w0 = ((int64_t)j * kPlanThreads + tid) * stretch;
+      uint32_t k = sums[j * kPlanThreads + tid];
+      if (k >= num_new) break;
+      int row = last_at_most(first, a.R, k);
+      uint32_t next = row + 1 < a.R ? first[row + 1] : kSat;
+      int32_t* entry = a.tables + row * a.table_ld + blocks_in(a, past[row]) + (k - first[row]);
+#pragma unroll 1
+      for (int64_t w = w0; w < w0 + stretch && w < words && k < num_new; ++w) {
+        for (uint32_t mine = a.free[w] & plan_mask(a, w); mine != 0 && k < num_new; mine &= mine - 1u) {
+          if (k >= next) {
+            do {
+              ++row;
+              next = row + 1 < a.R ? first[row + 1] : kSat;
+            } while (k >= next);
+            entry = a.tables + row * a.table_ld + blocks_in(a, past[row]);
+          }
+          *entry++ = (int32_t)(32 * w) + __ffs(mine) - 1;
+          ++k;
+        }
+      }
     }
   }
   if (num_new > 0) __syncthreads();  // tables are written, and the bitmap is read: it may be written now

@@ -141,6 +141,31 @@ def test_plan_takes_the_lowest_free_pages(num_pages, where):
         assert np.array_equal(got[4], want[4])
 
 
+@pytest.mark.parametrize("num_pages", [20_000, 262_144, 300_000, 2_000_003])
+@pytest.mark.parametrize("R", [1, 37, 1025, 8192])
+@pytest.mark.parametrize("density", [0.02, 0.5, 1.0])
+def test_plan_of_many_pages(num_pages, R, density):
+    """More pages than are looked for one by one, for rows with many, with one and with none."""
+    rng = np.random.default_rng(R + num_pages)
+    free = rng.random(num_pages) < density
+    total = min(int(free.sum()), 17_000)
+    cut = np.sort(rng.integers(0, total + 1, R - 1))
+    new = np.diff(np.concatenate([[0], cut, [total]]))
+    blocks = int(new.max()) + 3
+    past = rng.integers(0, 4, R)
+    tables = np.full((R, blocks), -1, dtype=np.int32)
+    for take in {True, total < int(free.sum())}:  # exactly what there is, or some are left
+        some = free.copy()
+        if take:
+            some[np.flatnonzero(free)[total:]] = False
+        tables[:] = -1
+        want = plan_reference(past.tolist(), new.tolist(), tables, some, 1, total + 1)
+        got = run_plan(past, new, tables, some, num_pages, 1, total + 1, apart=not take)
+        assert status() == 0
+        for name, g, w in zip(("cu", "start", "lens", "positions", "slots", "tables", "free"), got, want):
+            assert np.array_equal(g, np.asarray(w)), name
+
+
 def test_plan_leaves_bits_behind_the_pool():
     words = dev([-1, -1])
     t = torch.full((1, 40), -1, dtype=I32, device="cuda")
