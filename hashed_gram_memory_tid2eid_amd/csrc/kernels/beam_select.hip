@@ -173,9 +173,10 @@ struct Logits<uint16_t> {  // bf16
 __device__ __forceinline__ float one_logit(const float* x, int e) { return x[e]; }
 __device__ __forceinline__ float one_logit(const uint16_t* x, int e) { return __uint_as_float((uint32_t)x[e] << 16); }
 
-// What a piece whose maximum is m takes off its exponents (in powers of two).
-constexpr float kFar = 1099511627776.0f;  // 2^40
-__device__ __forceinline__ float select_center(float m) { return fabsf(m) < kFar ? m * kLog2e : 0.0f; }
+// A piece whose maximum m is below kFar takes the float next to m log2e off its exponents (in powers
+// of two), and is off by its rounding, at most 2^-14, whose square is left out of the correction.
+constexpr float kFar = 1024.0f;
+__device__ __forceinline__ float select_center(float m) { return m * kLog2e; }
 
 // Beams whose logits are not read: done, or without a finite score.
 __device__ __forceinline__ bool beam_is_live(const SelectArgs& a, int row) {
@@ -239,10 +240,10 @@ __global__ __launch_bounds__(kSelectThreads, Logits<T>::kWaves) void beam_select
   const float bound = reach <= in_order(kLowest) ? kLowest : from_order(reach);
 
   // exp(x - m) as 2^(x log2e - c), c the float next to m log2e: one fma, rounded by 2^-24 of the
-  // exponent; the merge makes up for c's own rounding.  (Far from zero only x = m counts: the
-  // next float is 2^16 or more away.)
+  // exponent; the merge makes up for c's own rounding.  Far from zero, as 2^((x - m) log2e).
   const float c = select_center(m);
   const bool far = fabsf(m) >= kFar;
+  const float base = m == -INFINITY ? 0.0f : m;
   float sum[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -258,7 +259,7 @@ __global__ __launch_bounds__(kSelectThreads, Logits<T>::kWaves) void beam_select
       for (int i = 0; i < kVec; ++i) sum[i & 1] += __builtin_amdgcn_exp2f(__builtin_fmaf(v[j].at(i), kLog2e, -c));
     } else {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) sum[i & 1] += v[j].at(i) == m ? 1.0f : 0.0f;
+      for (int i = 0; i < kVec; ++i) sum[i & 1] += __builtin_amdgcn_exp2f((v[j].at(i) - base) * kLog2e);
     }
   }
   const float s = sum_of_wave(sum[0] + sum[1]);
@@ -387,7 +388,7 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
         for (int i = lane; i < S; i += 64) {
           if (i >= 64) p = part[i];
           // a piece's sum is of 2^(x log2e - c), with the constant as fp32 has it
-          const double shift = (double)select_center(p.x) - (fabsf(p.x) < kFar ? (double)p.x * (double)kLog2e : 0.0);
+          const double shift = fabsf(p.x) < kFar ? (double)select_center(p.x) - (double)p.x * (double)kLog2e : 0.0;
           const float scale = __builtin_amdgcn_exp2f((p.x - m) * kLog2e);
           z += (double)p.y * (double)scale * (1.0 + shift * 0.6931471805599453);
         }

@@ -707,9 +707,9 @@ int engram_block_release(const int32_t* d_tables, int64_t table_ld, int32_t max_
  * end_token with its score unchanged.  No candidates: a logit of -inf; a beam whose score is
  * not finite (its logits are not read), or whose logits hold a NaN or +inf, or are all -inf.
  * Where a request has fewer than n candidates the rest is token -1, parent -1, score -inf,
- * done 0.  Exponentials and their sums over a lane's part of the vocabulary are fp32, all sums
- * above fp32 pairs and the totals 64 bits, so that totals are off by about 1e-7 times the
- * logits' spread before their one rounding.
+ * done 0.  Exponentials and their sums over pieces of the vocabulary (up to 16,384 logits) are
+ * fp32, the pieces' sum, its logarithm and the totals 64 bits: before its one rounding a total
+ * is off by some 1e-7.
  *   BF16 or F32 logits, rows aligned to their element, ld >= V,
  *   1 <= V <= 2^24, 1 <= K, n <= 64, G >= 0, G * K <= 2^20; d_done and d_out_done may be NULL;
  *   end_token in [0, V), or -1 for none (d_done then NULL); out_scores may be the scores and

@@ -462,6 +462,25 @@ def test_select_lowest_values_and_wide_ranges(dtype):
     assert [int(v) for p, v in zip(parents[2], tokens[2]) if p == 0] == [777]
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("offset", [-1000.0, 700.0, 1023.0, 1025.0, 4097.0, 3e4, -1e5, 1e6, 3e8, -2e12, 1e20, 1e37])
+def test_select_logits_far_from_zero(offset, dtype):
+    """exp(x - most) where logits are large and their differences are not (float32 keeps fewer of them;
+    bf16 keeps few that differ at all)."""
+    x, scores = select_inputs(12, 3, 4, 20_001)
+    check_select(x + offset, scores, None, -1, 8, dtype)
+
+
+@pytest.mark.parametrize("V", [4096, 129_280])
+def test_select_pieces_of_different_sizes(V):
+    """Pieces whose maxima are far apart, on both sides of where exponents are taken differently."""
+    x, scores = select_inputs(13, 2, 3, V)
+    x[:, : V // 2] += 1030.0
+    x[1, : V // 4] -= 3000.0
+    x[2, V // 3:] -= 1e30
+    check_select(x, scores, None, -1, 8, torch.float32)
+
+
 def test_select_orders_a_beam_by_its_logits():
     """Steps of float32's last bit, in rising and falling order, with a list that starts full."""
     base = np.float32(7.0)
