@@ -22,6 +22,9 @@
  *                             sequence, continuing from the store) in one launch.
  *   engram_store_*            the rolling store: reset, write, read (snapshot)
  *                             and rollback to accepted lengths.
+ *   engram_block_*,           what a serving loop needs around the store: block
+ *   engram_beam_*,            tables and slot maps from request lengths, beam
+ *   engram_state_copy         search's selection, and the states that follow it.
  *   One layout may describe several Engram sites sharing one hash pass; the
  *   gathers then take a site index.  Tables may live in HBM or in pinned host
  *   memory (engram_host_device_pointer).
