@@ -104,6 +104,7 @@ def engram_beam_select(logits, scores, tokens, parents, out_scores, *, workspace
         raise ValueError("tokens, parents and out_scores must be [G][n]")
     _need(done_out is None or done_out.shape == shape, "done_out must be [G][n]")
     _need(done is None or done.shape == scores.shape, "done must be [G][K]")
+    end_token = int(end_token)
     _need(-1 <= end_token < 1 << 31, "end_token must be a token or -1")
     _count(rows, "G * K"), _count(V, "V")
     _check(_lib.engram_beam_select(

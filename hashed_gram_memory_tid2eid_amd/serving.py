@@ -99,8 +99,8 @@ class BeamDecode:
         G, K, P = self.requests, self.beams, self.page_size
         if self._started:
             raise RuntimeError("the last prompts' beams still hold their pages: call finish first")
-        if tuple(lens.shape) != (G,) or lens.dtype != torch.int32:
-            raise ValueError("lens must be int32 [requests]")
+        if tuple(lens.shape) != (G,) or lens.dtype != torch.int32 or not lens.is_cuda:
+            raise ValueError("lens must be int32 [requests] on the device")
         if not 0 <= num_tokens <= self.max_prompt_tokens:
             raise ValueError(f"{num_tokens} tokens, max_prompt_tokens is {self.max_prompt_tokens}")
         self._started = True

@@ -226,7 +226,7 @@ def test_construction_refuses():
     with pytest.raises(ValueError):
         eng.BeamDecode(None, caches=[torch.zeros((3, 2), device="cuda")], **ok)
     d = eng.BeamDecode(None, **ok)
-    for lens, n in ((dev([1]), 2), (dev([1, 1], torch.int64), 2), (dev([1, 1]), 17), (dev([1, 1]), -1)):
+    for lens, n in ((dev([1]), 2), (dev([1, 1], torch.int64), 2), (dev([1, 1]), 17), (dev([1, 1]), -1), (dev([1, 1]).cpu(), 2)):
         with pytest.raises(ValueError):
             d.start(lens, n)
     d.start(dev([1, 1]), 2)
