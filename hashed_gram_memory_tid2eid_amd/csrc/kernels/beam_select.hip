@@ -6,15 +6,19 @@
 // Two launches.  The first cuts every row of logits into pieces of 256 lanes x NV loads of 16
 // bytes, one workgroup each, and reads each logit once: a piece stays in registers while its
 // maximum m is found, then its sum of exp(x - m) and its n largest logits.  Those need no sort
-// of the piece: lane i of the four waves stands for the maximum of its elements, and a bound
-// that n of these 64 maxima reach is reached by n elements at least and by few more.  The loads
-// that hold such an element go to a list in LDS whole, the elements in them that reach the bound
-// to a second one, and there each finds its rank by counting the larger ones.  Keys of (logit,
-// lowest token first) are all different, so ranks are, too, whatever the order in which the
-// lists were filled.  Lists that overflow (many equal logits) are not used; the piece's n
-// largest are then taken one by one.
+// of the piece: lane i of the four waves stands for the maximum of its elements (or each of the
+// 256 threads for its own), and a bound that n of these maxima reach is reached by n elements at
+// least and by few more.  The loads that hold such an element go to a list in LDS whole, the
+// elements in them that reach the bound to a second one, and there each finds its rank by
+// counting the larger ones.  Keys of (logit, lowest token first) are all different, so ranks
+// are, too, whatever the order in which the lists were filled.  Lists that overflow (many equal
+// logits) are not used; the piece's n largest are then taken one by one.
 // The second launch, one workgroup a request, adds the pieces' sums in 64 bits, turns the keys
 // into totals and selects among them by the same bound, list and count.
+//
+// Bound by memory where rows are many (2,048 x 129,280 fp32: 152 us, 7.0 TB/s in the first launch;
+// bf16 85 us, 5.6 TB/s), by latency below (4 rows 8.4 us, 512 rows of 65,537 bf16 22.5: their
+// pieces all load, then all compute).
 
 namespace engram {
 
@@ -195,10 +199,10 @@ __device__ __forceinline__ bool beam_is_live(const SelectArgs& a, int row) {
   return (a.done == nullptr || a.done[row] == 0) && isfinite(a.scores[row]);
 }
 
-// Logits are read past the caches (2,048 rows of 129,280 fp32: 175 -> 157 us).  bf16 is bound
-// by its exponentials and runs 8 waves a SIMD: 64 registers, and 8 workgroups' lists in a CU's
-// LDS; fp32 by memory, where 5 workgroups, which is what its lists leave, read faster than 8
-// (154 against 157 us; bf16, 512 rows of 65,537: 26 against 24).
+// Logits are read past the caches (2,048 rows of 129,280 fp32: 175 -> 157 us).  bf16 runs 8 waves
+// a SIMD: 64 registers, and 8 workgroups' lists in a CU's LDS; fp32 has twice the loads to list,
+// which leave 5 workgroups, and these read faster than 8 (154 against 157 us; bf16 by 5, 512 rows
+// of 65,537: 26 against 24).
 template <typename T, int NV>
 __global__ __launch_bounds__(kSelectThreads, Logits<T>::kWaves) void beam_select_rows_kernel(SelectArgs a) {
   constexpr int kVec = Logits<T>::kVec, kSelectLoads = kSelectHeld / kVec;

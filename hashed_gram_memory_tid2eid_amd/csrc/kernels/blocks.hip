@@ -84,7 +84,7 @@ __device__ __forceinline__ uint32_t count_words(const PlanArgs& a, int64_t w, in
   if (w + kPlanWords < words) {
 #pragma unroll
     for (int i = 0; i < kPlanWords; ++i) sum += (uint32_t)__popc(v[i]);
-  } else {
+  } else if (w < words) {
 #pragma unroll
     for (int i = 0; i < kPlanWords; ++i) sum += (uint32_t)__popc(v[i] & plan_mask(a, w + i));
   }
@@ -100,9 +100,12 @@ __device__ __forceinline__ void load_words(const PlanArgs& a, int64_t w, int64_t
       const words_t v = *reinterpret_cast<const words_t*>(a.free + w + i);
       out[i] = v.x, out[i + 1] = v.y, out[i + 2] = v.z, out[i + 3] = v.w;
     }
-  } else {
+  } else if (w < words) {
 #pragma unroll
     for (int i = 0; i < kPlanWords; ++i) out[i] = w + i < words ? a.free[w + i] : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPlanWords; ++i) out[i] = 0u;
   }
 }
 
@@ -210,7 +213,7 @@ __global__ __launch_bounds__(kPlanThreads) void block_plan_kernel(PlanArgs a) {
     need[r] = blocks_in(a, p[r] + n[r]) - have;
     in[r] = n[r];
     in[ROWS + r] = need[r];
-    if (have > block) page[r] = a.tables[((int64_t)r * kPlanThreads + tid) * a.table_ld + block];
+    if (have > block && a.tokens_here) page[r] = a.tables[((int64_t)r * kPlanThreads + tid) * a.table_ld + block];
   }
 
   // one scan of all of them
