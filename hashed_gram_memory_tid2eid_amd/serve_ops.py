@@ -161,7 +161,7 @@ def engram_state_copy(state, src, dst, *, stream=None):
     planes, plane = 1, 0
     if len(shape) == 3 and shape[0] != 1:
         planes, plane = shape[0], strides[0]
-        _need(planes == 0 or plane >= (rows - 1) * pitch + width or pitch >= (planes - 1) * plane + width > width,
+        _need(planes == 0 or plane >= (rows - 1) * pitch + width or (plane >= width and pitch >= (planes - 1) * plane + width),
               "state must not have overlapping planes")
     n = _count(src.numel(), "n")
     _need(dst.numel() == n, "src and dst must be of one size")

@@ -693,6 +693,20 @@ def test_copy_of_interleaved_planes():
         eng.engram_state_copy(state[:1].expand(3, 4, 8), dev([1]), dev([2]))
 
 
+@pytest.mark.parametrize("shape, strides, good", [((2, 4, 8), (4, 32, 1), False), ((2, 4, 8), (8, 15, 1), False),
+                                                  ((2, 4, 8), (31, 8, 1), False), ((2, 4, 8), (8, 16, 1), True),
+                                                  ((2, 4, 8), (32, 8, 1), True), ((2, 4, 8), (9, 17, 1), True)])
+def test_copy_takes_planes_that_do_not_overlap(shape, strides, good):
+    state = torch.zeros(256, dtype=I32, device="cuda").as_strided(shape, strides)
+    if good:
+        state[:, 1] = 5
+        eng.engram_state_copy(state, dev([1]), dev([2]))
+        assert (state[:, 1:3] == 5).all() and int(state.sum()) == 160 and status() == 0
+    else:
+        with pytest.raises(ValueError):
+            eng.engram_state_copy(state, dev([1]), dev([2]))
+
+
 def test_copy_skips_rows_that_are_not_there():
     state = torch.arange(12, device="cuda", dtype=I32).view(3, 4)
     want = state.clone()
