@@ -119,6 +119,10 @@ class BeamDecode:
         engram_block_plan(first, lens.contiguous(), self.tables.view(G, K * self.blocks)[:, :self.blocks], self.free,
                           cu_seqlens=self.cu_seqlens, token_slots=self.token_slots, positions=self.positions,
                           seq_start=self.seq_start[:G], **pool)
+        with _on(stream):
+            # the other beams name the prompt's blocks, too, so that finish may follow at once
+            tables = self.tables.view(G, K, self.blocks)
+            tables[:, 1:] = tables[:, :1]
         engram_block_plan(self._past[:G * K], self._new[:G * K], self.tables, self.free, cu_seqlens=self._tail_cu,
                           token_slots=self._tail_slots, lens=self.lens, **pool)
 

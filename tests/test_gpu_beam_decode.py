@@ -217,6 +217,17 @@ def test_pool_that_runs_out_leaves_the_beams_as_they_were():
     assert all(torch.equal(a, b) for a, b in zip(state, (d.tables, d.free, d.lens)))
 
 
+@pytest.mark.parametrize("lens", [[1, 2], [4, 5], [9, 12]])
+def test_prompts_that_are_given_up_leave_no_fault(lens):
+    """finish right after start: full blocks of the prompts are named by every beam."""
+    d = eng.BeamDecode(None, requests=2, beams=3, max_len=16, page_size=4, vocab=10)
+    for _ in range(2):
+        d.start(dev(lens), sum(lens))
+        d.finish()
+        assert eng.engram_get_error() == 0
+        assert unpack(d.free.cpu(), d.num_pages).all()
+
+
 def test_construction_refuses():
     ok = dict(requests=2, beams=2, max_len=8, page_size=2, vocab=10)
     for change in (dict(requests=0), dict(beams=0), dict(beams=65), dict(max_len=0), dict(page_size=0),
