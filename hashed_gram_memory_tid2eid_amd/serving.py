@@ -34,7 +34,7 @@ class BeamDecode:
     alone.  ``caches``: tensors [pages][width] or [layers][pages][width] whose rows are the pool's
     pages; they are copied where beams part inside a page.  ``num_pages`` defaults to a whole
     table for every beam; it may be less, since the beams of a request share what they have in
-    common.
+    common.  ``stream``: that of the first calls, behind all that the current stream holds.
 
     Buffers on the device: tokens, parents, slots, scores, done [requests][beams]; lens and tables,
     a row a beam; free, the pool.  Of the last plan: cu_seqlens, seq_start, token_slots and
@@ -85,6 +85,12 @@ class BeamDecode:
         self._each = torch.arange(n + 1, **i32)
         self._started = False
         self._rows_planned(0, 0)
+        if stream is not None:
+            # the buffers belong to the current stream: what it fills them with comes before the
+            # first call on `stream`
+            here = torch.cuda.current_stream()
+            with _on(stream):
+                torch.cuda.current_stream().wait_stream(here)
 
     def _rows_planned(self, rows, tokens):
         self.cu_seqlens = self._cu[:rows + 1]
@@ -114,9 +120,9 @@ class BeamDecode:
             past.copy_(lens[:, None]).sub_(new)
             self.lens.zero_()
             self.done.zero_()
-            first = self.lens.view(G, K)[:, 0].contiguous()
+            first, lens = self.lens.view(G, K)[:, 0].contiguous(), lens.contiguous()
         self._rows_planned(G, num_tokens)
-        engram_block_plan(first, lens.contiguous(), self.tables.view(G, K * self.blocks)[:, :self.blocks], self.free,
+        engram_block_plan(first, lens, self.tables.view(G, K * self.blocks)[:, :self.blocks], self.free,
                           cu_seqlens=self.cu_seqlens, token_slots=self.token_slots, positions=self.positions,
                           seq_start=self.seq_start[:G], **pool)
         with _on(stream):

@@ -307,6 +307,38 @@ def test_steps_on_another_stream_and_in_a_graph():
     assert eng.engram_get_error() == 0
 
 
+def test_a_busy_current_stream_is_waited_for_only_where_it_is_needed():
+    """Made for another stream: buffers are filled before its first call.  Lengths that are a strided
+    view are made contiguous on the call's stream, not behind what the current one still does."""
+    def state(d):
+        return [t.clone() for t in (d.tokens, d.parents, d.scores, d.slots, d.lens, d.tables, d.free, d.token_slots,
+                                    d.positions, d.cu_seqlens, d.seq_start)]
+
+    size = dict(requests=3, beams=2, max_len=64, page_size=4, vocab=1000)
+    logits = torch.randn((3, 1000), device="cuda")
+    lens = dev([5, 99, 8, 99, 3, 99])[::2]
+    work = torch.ones((8192, 8192), device="cuda")
+    d = eng.BeamDecode(None, **size)
+    d.start(lens, 16)
+    d.first(logits)
+    want = state(d)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        work @ work
+    d = eng.BeamDecode(None, stream=side, **size)
+    side.synchronize()
+    for _ in range(4):
+        work @ work
+    d.start(lens, 16, stream=side)
+    d.first(logits, stream=side)
+    with torch.cuda.stream(side):
+        got = state(d)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert eng.engram_get_error(side) == 0
+
+
 def test_selections_at_the_same_time():
     """Two streams, a workspace each."""
     G, K, V, n = 8, 4, 40_000, 8
