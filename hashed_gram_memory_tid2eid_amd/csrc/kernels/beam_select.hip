@@ -17,7 +17,7 @@
 // into totals and selects among them by the same bound, list and count.
 //
 // Bound by memory where rows are many (2,048 x 129,280 fp32: 152 us, 7.0 TB/s in the first launch;
-// bf16 85 us, 5.6 TB/s), by latency below (4 rows 8.4 us, 512 rows of 65,537 bf16 22.5: their
+// bf16 80 us, 6.0 TB/s), by latency below (4 rows 8.8 us, 512 rows of 65,537 bf16 22.2: their
 // pieces all load, then all compute).
 
 namespace engram {
