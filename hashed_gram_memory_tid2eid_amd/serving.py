@@ -100,7 +100,10 @@ class BeamDecode:
         """Pages for prompts of ``lens`` int32 [requests] tokens, each at least one, held by every
         request's first beam, and a last page for each of its other beams.  num_tokens: places
         for the prompts' tokens, at least their sum.  Afterwards cu_seqlens [requests + 1],
-        token_slots, positions and seq_start are those of the prompts."""
+        token_slots, positions and seq_start are those of the prompts.  A fault is latched: prompts
+        that do not fit (their pages, num_tokens, max_len) take nothing and every length is 0;
+        where only the last pages do not fit, the first beams hold the prompts and the others
+        their full blocks.  finish follows either way."""
         import torch
         G, K, P = self.requests, self.beams, self.page_size
         if self._started:
@@ -112,20 +115,21 @@ class BeamDecode:
         self._started = True
         pool = dict(page_size=P, num_pages=self.num_pages, stream=stream)
         with _on(stream):
-            past, new = self._past[:G * K].view(G, K), self._new[:G * K].view(G, K)
-            tail = lens.remainder(P)
-            new.zero_()
-            if K > 1:
-                new[:, 1:] = tail[:, None]
-            past.copy_(lens[:, None]).sub_(new)
             self.lens.zero_()
             self.done.zero_()
-            first, lens = self.lens.view(G, K)[:, 0].contiguous(), lens.contiguous()
+            held, lens = self.lens.view(G, K)[:, 0].contiguous(), lens.contiguous()
         self._rows_planned(G, num_tokens)
-        engram_block_plan(first, lens, self.tables.view(G, K * self.blocks)[:, :self.blocks], self.free,
+        engram_block_plan(held, lens, self.tables.view(G, K * self.blocks)[:, :self.blocks], self.free,
                           cu_seqlens=self.cu_seqlens, token_slots=self.token_slots, positions=self.positions,
-                          seq_start=self.seq_start[:G], **pool)
+                          seq_start=self.seq_start[:G], lens=held, **pool)
         with _on(stream):
+            # from here on the lengths that were granted: 0 after a fault, when the tables still
+            # name pages of earlier prompts
+            past, new = self._past[:G * K].view(G, K), self._new[:G * K].view(G, K)
+            new.zero_()
+            if K > 1:
+                new[:, 1:] = held.remainder(P)[:, None]
+            past.copy_(held[:, None]).sub_(new)
             # the other beams name the prompt's blocks, too, so that finish may follow at once
             tables = self.tables.view(G, K, self.blocks)
             tables[:, 1:] = tables[:, :1]

@@ -1,0 +1,75 @@
+"""BeamDecode after a fault: what a start or a plan that does not fit leaves behind, on states that
+have served other prompts before."""
+import pytest
+import torch
+
+from test_gpu_serve_ops import dev, status, unpack
+
+pytestmark = pytest.mark.gpu
+
+eng = pytest.importorskip("hashed_gram_memory_tid2eid_amd")
+
+
+def used_before(K, num_pages):
+    """Two requests over pages of 4 tokens, whose tables name pages of earlier prompts."""
+    d = eng.BeamDecode(None, requests=2, beams=K, max_len=20, page_size=4, vocab=10, num_pages=num_pages)
+    d.start(dev([8, 4]), 12)
+    d.finish()
+    assert status() == 0
+    return d
+
+
+def all_free(d):
+    return unpack(d.free.cpu(), d.num_pages).all()
+
+
+@pytest.mark.parametrize("K", [1, 3])
+@pytest.mark.parametrize("lens, places, code", [
+    ([12, 13], 25, "PAGES"),          # seven pages of six
+    ([6, 7], 12, "SEQLENS"),          # a token more than places
+    ([6, -1], 30, "SEQLENS"), ([6, 21], 30, "SEQLENS"),
+])
+def test_start_of_prompts_that_do_not_fit_takes_nothing(K, lens, places, code):
+    d = used_before(K, 6)
+    d.start(dev(lens), places)
+    assert status() == eng.STATUS["ENGRAM_E_" + code]
+    assert d.lens.tolist() == [0] * (2 * K) and all_free(d)
+    assert d.cu_seqlens.tolist() == [0] * 3 and (d.token_slots == -1).all()
+    # rows that hold nothing: a token of each lies on a page of its own
+    d.plan()
+    assert status() == 0
+    slots = d.token_slots.tolist()
+    assert len(set(slots)) == 2 * K and min(slots) >= 0 and d.positions.tolist() == [0] * (2 * K)
+    d.finish()
+    assert status() == 0 and all_free(d)
+    d.start(dev([8, 4]), 12)
+    assert status() == 0 and d.lens.tolist() == [8] * K + [4] * K
+
+
+@pytest.mark.parametrize("lens", [[8, 5], [9, 10], [1, 1]])
+def test_start_whose_last_pages_do_not_fit(lens):
+    """The first beams have their prompts, the others no page of their own; finish gives all of it back."""
+    K, own = 3, sum(-(-n // 4) for n in lens)
+    d = used_before(K, max(own, 5))
+    d.start(dev(lens), sum(lens))
+    assert status() == eng.ENGRAM_E_PAGES
+    assert d.lens.view(2, K).tolist() == [[n] + [n // 4 * 4] * (K - 1) for n in lens]
+    assert int(unpack(d.free.cpu(), d.num_pages).sum()) == d.num_pages - own
+    d.finish()
+    assert status() == 0 and all_free(d)
+
+
+def test_start_that_fits_again_after_a_fault():
+    d = used_before(2, 6)
+    for _ in range(2):
+        d.start(dev([13, 12]), 25)
+        assert status() == eng.ENGRAM_E_PAGES
+        d.finish()
+        d.start(dev([6, 3]), 9)
+        assert status() == 0 and d.lens.tolist() == [6, 6, 3, 3]
+        assert int(unpack(d.free.cpu(), d.num_pages).sum()) == 6 - 5
+        tables = d.tables.tolist()
+        last = [tables[r][n // 4] for r, n in enumerate(d.lens.tolist())]
+        assert len(set(last)) == 4 and tables[0][0] == tables[1][0]
+        d.finish()
+        assert status() == 0 and all_free(d)
