@@ -56,8 +56,6 @@ class BeamDecode:
         self.blocks = -(-max_len // page_size)
         self.num_pages = n * self.blocks if num_pages is None else int(num_pages)
         self.end_token, self.caches = end_token, list(caches)
-        if any(c.shape[-2] < self.num_pages for c in self.caches):
-            raise ValueError("a cache has fewer pages than the pool")
         self.max_prompt_tokens = G * max_len if max_prompt_tokens is None else int(max_prompt_tokens)
         places = max(self.max_prompt_tokens, n)
         i32 = dict(dtype=torch.int32, device="cuda")
@@ -68,6 +66,12 @@ class BeamDecode:
         bits = torch.arange(-(-self.num_pages // 32) * 32, device="cuda").view(-1, 32) < self.num_pages
         self.free = (bits.long() << torch.arange(32, device="cuda")).sum(1).to(torch.uint32).view(torch.int32)
         self.tokens, self.parents, self.page_src, self.page_dst = (torch.zeros((G, K), **i32) for _ in range(4))
+        for c in self.caches:
+            # a copy of no row, whose refusals would otherwise come at the first selection, when
+            # the beams have moved
+            engram_state_copy(c, self.page_src, self.page_dst)
+            if c.shape[-2] < self.num_pages:
+                raise ValueError("a cache has fewer pages than the pool")
         self.scores = torch.zeros((G, K), dtype=torch.float32, device="cuda")
         self.done = torch.zeros((G, K), dtype=torch.uint8, device="cuda")
         self.seq_start = torch.zeros(n, dtype=torch.uint8, device="cuda")

@@ -73,3 +73,23 @@ def test_start_that_fits_again_after_a_fault():
         assert len(set(last)) == 4 and tables[0][0] == tables[1][0]
         d.finish()
         assert status() == 0 and all_free(d)
+
+
+# ---------------------------------------------------------------------------
+# caches
+# ---------------------------------------------------------------------------
+
+def test_caches_that_cannot_be_copied_are_refused_when_made():
+    """Not at the first selection, whose beams have moved by then."""
+    size = dict(requests=2, beams=2, max_len=8, page_size=2, vocab=10)
+    zeros = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    for cache in (zeros(8), zeros(2, 2, 8, 4), zeros(4, 16).t(), zeros(1, 4).expand(16, 4), zeros(1, 16, 4).expand(2, 16, 4),
+                  zeros(2, 16, 4).cpu(), zeros(40).as_strided((2, 16, 2), (1, 2, 1))):
+        with pytest.raises((TypeError, ValueError)):
+            eng.BeamDecode(None, caches=[zeros(16, 4), cache], **size)
+    with pytest.raises(eng.EngramError):  # more planes than a copy of these beams takes
+        eng.BeamDecode(None, caches=[torch.zeros((1 << 22, 16, 1), dtype=torch.uint8, device="cuda")], **size)
+    d = eng.BeamDecode(None, caches=[zeros(16, 4), zeros(3, 17, 5), zeros(16, 2, 4).transpose(0, 1)], **size)
+    d.start(dev([1, 1]), 2)
+    d.first(torch.zeros((2, 10), device="cuda"))
+    assert status() == 0
