@@ -182,12 +182,29 @@ extern "C" int engram_beam_reorder(const int32_t* d_parents, int32_t G, int32_t 
   return engram::hip_error_status(engram::launch_beam_reorder(a, stream));
 }
 
+namespace {
+
+// `count` spans of `bytes`, `pitch` apart, end within `most` (all of them positive).
+bool spans_within(int64_t count, int64_t pitch, int64_t bytes, int64_t most) {
+  return most >= bytes && (count - 1 == 0 || pitch <= (most - bytes) / (count - 1));
+}
+
+// No byte is in two rows: planes whole one behind another, or rows whole with their planes inside.
+bool rows_apart(int64_t planes, int64_t plane_pitch, int64_t rows, int64_t row_pitch, int64_t row_bytes) {
+  if (planes <= 1 || rows == 0) return true;
+  return spans_within(rows, row_pitch, row_bytes, plane_pitch) ||
+         (plane_pitch >= row_bytes && spans_within(planes, plane_pitch, row_bytes, row_pitch));
+}
+
+}  // namespace
+
 extern "C" int engram_state_copy(void* d_state, int64_t planes, int64_t plane_pitch, int64_t rows, int64_t row_pitch,
                                  int64_t row_bytes, const int32_t* d_src, const int32_t* d_dst, int32_t n,
                                  hipStream_t stream) {
   if (planes < 0 || plane_pitch < 0 || rows < 0 || row_bytes < 1 || row_pitch < row_bytes || n < 0) return ENGRAM_E_ARG;
   if (rows > kMax32 || row_bytes > 65535 * 1024) return ENGRAM_E_UNSUPPORTED;  // that many pieces of single bytes
   if (planes > kMaxGroups || (int64_t)n * planes > kMaxGroups) return ENGRAM_E_UNSUPPORTED;
+  if (!rows_apart(planes, plane_pitch, rows, row_pitch, row_bytes)) return ENGRAM_E_ARG;
   if (n == 0 || planes == 0) return ENGRAM_OK;
   if (!d_state || !d_src || !d_dst) return ENGRAM_E_ARG;
   if (!aligned(d_src, 4) || !aligned(d_dst, 4)) return ENGRAM_E_ALIGN;

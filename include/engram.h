@@ -766,8 +766,11 @@ int engram_beam_reorder(const int32_t* d_parents, int32_t G, int32_t K, engram_s
  * (a cache's pages in every layer, or slot-keyed states).  A pair with -1 on either side, or
  * the same row on both, is none.  No row is a source and a destination, or a destination
  * twice; engram_beam_reorder names such pairs.
- *   planes, rows, n >= 0, rows < 2^31, planes * n < 2^24; 1 <= row_bytes < 2^26 - 1,024;
- *   row_pitch >= row_bytes; plane_pitch >= 0.  A state whose address, pitches and row_bytes are multiples of 16 is copied fastest.
+ *   planes, rows, n >= 0, rows < 2^31, planes * n < 2^24; 1 <= row_bytes <= 2^26 - 1,024;
+ *   row_pitch >= row_bytes; plane_pitch >= 0, and with more than one plane no byte lies in two
+ *   rows: plane_pitch >= (rows - 1) * row_pitch + row_bytes, or planes lie inside a row's pitch
+ *   (plane_pitch >= row_bytes and row_pitch >= (planes - 1) * plane_pitch + row_bytes).  A state
+ *   whose address, pitches and row_bytes are multiples of 16 is copied fastest.
  * Host errors: ENGRAM_E_ARG, ENGRAM_E_UNSUPPORTED.  Device error: ENGRAM_E_SLOT_RANGE (a row
  * outside [0, rows): that pair is skipped). */
 int engram_state_copy(void* d_state, int64_t planes, int64_t plane_pitch, int64_t rows, int64_t row_pitch,
