@@ -105,7 +105,8 @@ PyObject* address(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // matrix(t, name, dtype or None, dev): (address, rows, columns, leading dimension) of a matrix
-// whose rows are contiguous and do not overlap.
+// whose rows are contiguous and do not overlap.  Rows and columns fit the library's 32-bit
+// arguments: ctypes would cut them down without a word.
 PyObject* matrix(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     if (!wants(n, 4)) return nullptr;
@@ -119,6 +120,11 @@ PyObject* matrix(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return nullptr;
     }
     const int64_t rows = t->size(0), cols = t->size(1);
+    if (rows >> 31 != 0 || cols >> 31 != 0) {
+      PyErr_Format(PyExc_ValueError, "%s must have fewer than 2^31 rows and columns, got %lld x %lld", name, (long long)rows,
+                   (long long)cols);
+      return nullptr;
+    }
     if (cols > 1 && t->stride(1) != 1) {
       PyErr_Format(PyExc_ValueError, "%s must have contiguous rows", name);
       return nullptr;

@@ -94,7 +94,7 @@ def engram_beam_select(logits, scores, tokens, parents, out_scores, *, workspace
     dev = _place(scores, "scores")
     _need(scores.dim() == 2 and tokens.dim() == 2, "scores must be [G][K], tokens [G][n]")
     (G, K), shape = scores.shape, tokens.shape
-    n = shape[1]
+    n = _count(shape[1], "n")
     lp, rows, V, ld = _rows(logits, "logits", None, dev)
     kind = _LOGITS.get(logits.dtype)
     if kind is None:
@@ -106,7 +106,6 @@ def engram_beam_select(logits, scores, tokens, parents, out_scores, *, workspace
     _need(done is None or done.shape == scores.shape, "done must be [G][K]")
     end_token = int(end_token)
     _need(-1 <= end_token < 1 << 31, "end_token must be a token or -1")
-    _count(rows, "G * K"), _count(V, "V")
     _check(_lib.engram_beam_select(
         lp, kind, ld, G, K, V, _arg(scores, "scores", _F32, 0, dev), _arg(done, "done", _U8, 0, dev), end_token, n,
         _arg(tokens, "tokens", _I32, 0, dev), _arg(parents, "parents", _I32, 0, dev),
