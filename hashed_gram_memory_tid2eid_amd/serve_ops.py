@@ -17,16 +17,20 @@ from . import ENGRAM_DTYPE_BF16, ENGRAM_DTYPE_F32, _check, _lib, _need, _stream
 try:
     from ._tensor_args import address as _arg, device as _place, matrix as _rows
 except ImportError as e:
-    raise ImportError("_tensor_args.so is missing or does not fit this torch: build it with "
-                      "`python hashed_gram_memory_tid2eid_amd/build_lib.py`") from e
+    _absent = e
+
+    def _place(t, name):
+        """The first check of every operator here: without the module none of them can run."""
+        raise ImportError("_tensor_args.so is missing or does not fit this torch: build it with "
+                          "`python hashed_gram_memory_tid2eid_amd/build_lib.py`") from _absent
+
 
 _I32, _I64, _U8, _F32 = torch.int32, torch.int64, torch.uint8, torch.float32
 _LOGITS = {torch.bfloat16: ENGRAM_DTYPE_BF16, torch.float32: ENGRAM_DTYPE_F32}
-_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _raw(stream, dev):
-    return _raw_stream(dev) if stream is None else _stream(stream)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _count(n, name):
