@@ -4,13 +4,14 @@ Usage: ``python hashed_gram_memory_tid2eid_amd/build_lib.py`` (run by path: impo
 the package loads the library this script builds).  Compiles the single
 device translation unit and the host sources to objects under ``_build/`` and
 links ``hashed_gram_memory_tid2eid_amd/libengram.so``; beside it the Python binding's
-extension module ``_tensor_args.so`` with g++ against the installed torch.  Always
-recompiles.
+extension module ``_tensor_args`` with g++ against the installed torch, whose object
+layouts it inlines.  Always recompiles.
 
 The library carries a hash of what it was built from (every source under
 ``csrc/`` and ``include/`` plus the compiler flags), readable with
 ``engram_build_id()``.  ``ensure_built()`` rebuilds whenever that hash differs
-from the sources in the tree, so a stale library is never loaded.
+from the sources in the tree, so a stale library is never loaded.  The extension
+module records its source, flags, torch and Python in the same way.
 """
 from __future__ import annotations
 
@@ -19,13 +20,15 @@ import os
 import re
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libengram.so")
-TENSOR_ARGS = os.path.join(PKG, "_tensor_args.so")
+EXT_SUFFIX = sysconfig.get_config_var("EXT_SUFFIX")  # names the Python it is for
+TENSOR_ARGS = os.path.join(PKG, "_tensor_args" + EXT_SUFFIX)
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -40,6 +43,8 @@ COMMON = [
 SOURCES = ["engram_device.hip", "abi.cpp", "layout.cpp", "noalloc.cpp", "train.cpp", "serve.cpp"]
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_ID_PREFIX = "engram-src-sha256:"
+TENSOR_ARGS_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-shared", "-Wall"]
+TENSOR_ARGS_PREFIX = "tensor-args-sha256:"
 
 
 def source_hash() -> str:
@@ -65,23 +70,42 @@ def source_hash() -> str:
 def built_hash(lib: str = LIB):
     """The source hash recorded in a built library, or None (missing, or built
     before the hash existed)."""
-    if not os.path.exists(lib):
+    return _recorded(lib, BUILD_ID_PREFIX)
+
+
+def _recorded(path: str, prefix: str):
+    if not os.path.exists(path):
         return None
-    with open(lib, "rb") as f:
-        m = re.search(re.escape(BUILD_ID_PREFIX.encode()) + rb"([0-9a-f]{16})", f.read())
+    with open(path, "rb") as f:
+        m = re.search(re.escape(prefix.encode()) + rb"([0-9a-f]{16})", f.read())
     return m.group(1).decode() if m else None
 
 
+def tensor_args_identity() -> str:
+    """First 16 hex digits of a SHA-256 over what _tensor_args is built from and for: its
+    source, its flags, the torch and the Python."""
+    import torch
+    with open(os.path.join(CSRC, "tensor_args.cpp"), "rb") as f:
+        h = hashlib.sha256(f.read())
+    h.update("\0".join([*TENSOR_ARGS_FLAGS, str(torch.__version__), EXT_SUFFIX]).encode())
+    return h.hexdigest()[:16]
+
+
+def built_tensor_args(path: str = TENSOR_ARGS):
+    """The identity recorded in a built _tensor_args, or None."""
+    return _recorded(path, TENSOR_ARGS_PREFIX)
+
+
 def tensor_args_command(out: str):
-    """How _tensor_args.so is built: the torch libraries it names are those that `import torch`
+    """How _tensor_args is built: the torch libraries it names are those that `import torch`
     has loaded by the time it is imported."""
-    import sysconfig
     import torch
     from torch.utils import cpp_extension
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     includes = [x for path in cpp_extension.include_paths() for x in ("-isystem", path)]
-    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *includes,
-            "-I", sysconfig.get_paths()["include"], f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+    defines = [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DTENSOR_ARGS_TORCH="{torch.__version__}"',
+               f'-DTENSOR_ARGS_ID="{TENSOR_ARGS_PREFIX}{tensor_args_identity()}"']
+    return [os.environ.get("CXX", "g++"), *TENSOR_ARGS_FLAGS, *includes, "-I", sysconfig.get_paths()["include"], *defines,
             os.path.join(CSRC, "tensor_args.cpp"), "-o", out, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
@@ -154,10 +178,11 @@ def build_hbm_reference() -> str:
 
 
 def ensure_built() -> str:
-    """Builds the library when it is missing or was built from other sources than
-    the tree holds now (compared by the embedded source hash); otherwise leaves
-    the built one in place."""
-    if built_hash() == source_hash() and os.path.exists(TENSOR_ARGS):
+    """Builds the library and the binding's extension module when one of them is
+    missing or was built from other sources than the tree holds now, or the module
+    for another torch or Python (compared by what is embedded in them); otherwise
+    leaves the built ones in place."""
+    if built_hash() == source_hash() and built_tensor_args() == tensor_args_identity():
         return LIB
     return build()
 

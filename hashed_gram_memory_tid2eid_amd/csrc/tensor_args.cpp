@@ -149,4 +149,14 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_args", "Checked addresses 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tensor_args() { return PyModule_Create(&module); }
+// TENSOR_ARGS_TORCH is the torch it was built for, with which alone it is used; TENSOR_ARGS_ID a hash of
+// everything it was built from and for.
+PyMODINIT_FUNC PyInit__tensor_args() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && (PyModule_AddStringConstant(m, "torch_version", TENSOR_ARGS_TORCH) != 0 ||
+            PyModule_AddStringConstant(m, "build_id", TENSOR_ARGS_ID) != 0)) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -15,13 +15,15 @@ import torch
 from . import ENGRAM_DTYPE_BF16, ENGRAM_DTYPE_F32, _check, _lib, _need, _stream
 
 try:
-    from ._tensor_args import address as _arg, device as _place, matrix as _rows
+    from ._tensor_args import address as _arg, device as _place, matrix as _rows, torch_version as _torch
+    if _torch != torch.__version__:  # it inlines that torch's object layouts
+        raise ImportError(f"it was built for torch {_torch}, this is {torch.__version__}")
 except ImportError as e:
     _absent = e
 
     def _place(t, name):
         """The first check of every operator here: without the module none of them can run."""
-        raise ImportError("_tensor_args.so is missing or does not fit this torch: build it with "
+        raise ImportError("the extension module _tensor_args is missing or does not fit this torch: build it with "
                           "`python hashed_gram_memory_tid2eid_amd/build_lib.py`") from _absent
 
 
