@@ -1,0 +1,106 @@
+"""Which candidates a selection takes, at every rank and the last one too: token, parent and done flag
+against a reference that lists candidates past the cut."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_serve_ops import SELECTS, run_select, select_inputs, select_reference, status
+
+pytestmark = pytest.mark.gpu
+
+eng = pytest.importorskip("hashed_gram_memory_tid2eid_amd")
+TYPES = [torch.bfloat16, torch.float32]
+PAST = 64  # candidates listed behind the cut
+
+
+def check_ranks(x, scores, done, end, n, dtype, **how):
+    """A kernel's total is off by tol at most (its derivation: the exponentials' differences to the
+    largest logit, up to 104 where exp leaves fp32's range, take 2.5 roundings of 2^-24 and 2 units;
+    the fp32 sums of a lane, a wave and four waves 41), so two candidates can change places where
+    their totals are within 2 tol; those of one beam never, whose order is by logit and token."""
+    x = torch.as_tensor(x).to(dtype).double().numpy()
+    G, K = scores.shape
+    ref = select_reference(x, scores, done, end, n + PAST)
+    tokens, parents, out, out_done = run_select(x, scores, done, end, n, dtype, **how)
+    assert status() == 0
+    finite = x[np.isfinite(x)]
+    spread = min(104.0, float(finite.max() - finite.min())) if finite.size else 0.0
+    tol = 2.0 ** -24 * (2.5 * spread + 2 + 41)
+    for g in range(G):
+        own = {b: [v for _, c, v in ref[g] if c == b] for b in range(K)}
+        taken = {b: 0 for b in range(K)}
+        totals = np.array([t for t, _, _ in ref[g]])
+        for i in range(n):
+            b, v = int(parents[g, i]), int(tokens[g, i])
+            if i >= len(ref[g]):
+                assert (v, b, out[g, i], out_done[g, i]) == (-1, -1, -np.inf, 0)
+                continue
+            assert 0 <= b < K, (g, i)
+            # a beam's candidates come in its own order, none left out
+            assert v == own[b][taken[b]], (g, i)
+            taken[b] += 1
+            t, want_b, want_v = ref[g][i]
+            near = {ref[g][j][1] for j in np.flatnonzero(np.abs(totals - t) <= 2 * tol)}
+            if len(near) == 1:
+                assert (b, v) == (want_b, want_v), (g, i)
+            else:
+                assert b in near, (g, i)
+            assert out_done[g, i] == int(v == end or (done is not None and done[g, b] != 0)), (g, i)
+            assert abs(float(out[g, i]) - t) <= 2 * tol + 2.0 ** -24 * abs(t) * 1.01, (g, i)
+    return tokens, parents, out, out_done
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("G, K, V, n", SELECTS + [(9, 1, 129_280, 1), (300, 1, 4097, 1), (33, 4, 20_001, 1), (40, 8, 65_536, 8)])
+def test_every_rank(G, K, V, n, dtype):
+    x, scores = select_inputs(G * 17 + V, G, K, V)
+    check_ranks(x, scores, None, min(V - 1, 3), n, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("masked", [0.3, 0.999])
+@pytest.mark.parametrize("n", [1, 7, 64])
+def test_every_rank_of_masked_rows_and_ended_beams(n, masked, dtype):
+    x, scores = select_inputs(n, 12, 5, 30_011, masked)
+    done = (np.random.default_rng(n).random((12, 5)) < 0.3).astype(np.uint8)
+    done[3] = 1
+    scores[5, 1:] = -np.inf
+    check_ranks(x, scores, done, 30_010, n, dtype)
+
+
+def crowded(kind, seed, G, K, V, dtype):
+    """Rows many of whose logits are equal or nearly so."""
+    rng = np.random.default_rng(seed)
+    x, scores = select_inputs(seed, G, K, V)
+    if kind.startswith("mask"):  # a finite number stands for a masked token
+        low = {"mask_lowest": torch.finfo(dtype).min, "mask_1e4": -1e4, "mask_zero": 0.0}[kind]
+        x = np.where(rng.random(x.shape) < 20 / V, np.abs(x) + 1.0, low)
+        x[0] = low                       # nothing is left of this row
+        x[1, :] = low
+        x[1, V - 1] = 1.0                # and one token of this
+    elif kind == "flat":                 # a model that has learnt nothing yet
+        x = -11.77 + 0.02 * rng.standard_normal(x.shape)
+    elif kind == "near":                 # float32's first 16 bits are the same for all
+        x = 5.0 + rng.integers(0, 1 << 14, x.shape) * 2.0 ** -21
+    elif kind == "steps":                # few values, each many times
+        x = np.floor(x)
+    elif kind == "signed_zeros":
+        x = np.where(rng.random(x.shape) < 0.5, -0.0, 0.0)
+        x[:, V // 2] = 1.0
+    elif kind == "zero_border":          # the smallest numbers on both sides of zero
+        x = rng.integers(-3000, 3000, x.shape) * 2.0 ** -149 if dtype == torch.float32 else np.floor(x) * 2.0 ** -133
+    elif kind == "highest":
+        x = np.where(rng.random(x.shape) < 0.9, torch.finfo(dtype).max, 0.0)
+    else:
+        x = np.full_like(x, 1.25)
+    return x, scores
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kind", ["mask_lowest", "mask_1e4", "mask_zero", "flat", "near", "steps", "signed_zeros", "zero_border",
+                                  "highest", "equal"])
+@pytest.mark.parametrize("G, K, V, n", [(2, 4, 129_280, 4), (3, 3, 4097, 64), (40, 4, 16_384, 16), (130, 8, 8193, 8), (1, 64, 9001, 64),
+                                        (520, 2, 8192, 5)])
+def test_every_rank_of_crowded_rows(G, K, V, n, kind, dtype):
+    x, scores = crowded(kind, n, G, K, V, dtype)
+    check_ranks(x, scores, None, -1, n, dtype)
