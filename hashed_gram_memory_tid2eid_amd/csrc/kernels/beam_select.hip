@@ -11,8 +11,11 @@
 // least and by few more.  The loads that hold such an element go to a list in LDS whole, the
 // elements in them that reach the bound to a second one, and there each finds its rank by
 // counting the larger ones.  Keys of (logit, lowest token first) are all different, so ranks
-// are, too, whatever the order in which the lists were filled.  Lists that overflow (many equal
-// logits) are not used; the piece's n largest are then taken one by one.
+// are, too, whatever the order in which the lists were filled.  Long lists are not ranked: many
+// logits are equal (masked by a finite number), or so near that the bound's 16 bits do not tell
+// fp32 ones apart (a flat row).  The bound is then raised by bisection, counting in the registers,
+// until few enough reach it or it is the n-th largest logit itself, whose equals follow those
+// above it by their tokens.
 // The second launch, one workgroup a request, adds the pieces' sums in 64 bits, turns the keys
 // into totals and selects among them by the same bound, list and count.
 //
@@ -24,8 +27,14 @@ namespace engram {
 
 constexpr int kSelectThreads = 256;
 constexpr int kSelectHeld = 4096;  // elements of the loads that hold one which reaches the bound
-constexpr int kSelectList = 1024;  // elements that reach it
+// Elements that reach it.  (Room past kSelectRanked leaves 5 workgroups of fp32 rows in a CU's LDS, which
+// read faster than more of them.)
+constexpr int kSelectList = 1024;
+// Up to so many are ranked (each reads all: 1,024 of them, in each of 1,024 elements of a mask's
+// value, took 210 us); 64 candidates leave some 75, so that ordinary rows are below it.
+constexpr int kSelectRanked = 128;
 constexpr int kFewLoads = 16;      // loads that one wave ranks; their elements cannot overflow the list
+static_assert(kFewLoads * 8 <= kSelectRanked && kSelectRanked <= kSelectList, "what one wave ranks is never too long");
 constexpr int kRankLanes = 8;      // lanes that count the larger ones of one element together
 // Up to so many of 64 values the n-th largest is a good bound: some 45 elements reach it where n
 // is 32.  All 64 are reached by hundreds, so more of them take 256 values (64 candidates of 64 x
@@ -108,6 +117,7 @@ __device__ __forceinline__ V of_wave(V v, V none, F f) {
 __device__ __forceinline__ float last_lane(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
+__device__ __forceinline__ int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
 __device__ __forceinline__ double last_lane(double v) {
   return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), 63), __builtin_amdgcn_readlane(__double2loint(v), 63));
 }
@@ -185,9 +195,6 @@ struct Logits<uint16_t> {  // bf16
   // half of the waves.
   __device__ __forceinline__ void again() { asm volatile("" : "+v"(raw)); }
 };
-
-__device__ __forceinline__ float one_logit(const float* x, int e) { return x[e]; }
-__device__ __forceinline__ float one_logit(const uint16_t* x, int e) { return __uint_as_float((uint32_t)x[e] << 16); }
 
 // A piece whose maximum m is below kFar takes the float next to m log2e off its exponents (in powers
 // of two), and is off by its rounding, at most 2^-14, whose square is left out of the correction.
@@ -299,7 +306,7 @@ __global__ __launch_bounds__(kSelectThreads, Logits<T>::kWaves) void beam_select
     else
       __syncthreads();
     const int reached = listed;
-    if (reached <= kSelectList) {
+    if (reached <= kSelectRanked) {
       for (int i = tid / kRankLanes; i < reached; i += workers / kRankLanes) {
         const unsigned long long key = list[i];
         int rank = 0;
@@ -311,28 +318,97 @@ __global__ __launch_bounds__(kSelectThreads, Logits<T>::kWaves) void beam_select
       return;
     }
   }
-  // too many equal ones: one by one from memory, each the largest key below the last
-  __shared__ unsigned long long wave_best[4];
-  unsigned long long last = ~0ull;
-  for (int r = 0; r < a.n; ++r) {
-    unsigned long long best = 0;
-    for (int e = first + tid; e < end; e += kSelectThreads) {
-      const float f = one_logit(x, e);
-      const unsigned long long key = select_key(f, e);
-      if (f >= kLowest && key < last && key > best) best = key;
+  // The bound for all 32 bits, again from the lanes' maxima: n elements at least reach lo, fewer
+  // reach hi.  Few may reach it by now; where it is a mask's value, it is the n-th largest itself.
+  if (!(m < INFINITY)) {  // a row without candidates
+    for (int i = tid; i < a.n; i += kSelectThreads) out[i] = 0;
+    return;
+  }
+  __shared__ int reached_by[2][4];
+  const uint32_t u0 = in_order(lane_max[0][lane]), u1 = in_order(lane_max[1][lane]), u2 = in_order(lane_max[2][lane]),
+                 u3 = in_order(lane_max[3][lane]);
+  uint32_t lo = a.n <= kFewCandidates ? bound_of_lanes(max(max(u0, u1), max(u2, u3)), a.n, 32)
+                                      : bound_of_four(u0, u1, u2, u3, a.n, 32);
+  lo = max(lo, in_order(kLowest));
+  uint32_t hi = in_order(m) + 1u, mid = lo;
+  bool few = false;
+  for (int step = 0; hi - lo > 1u && !few; ++step) {
+    const float t = from_order(mid);
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      v[j].again();
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) count += v[j].at(i) >= t ? 1 : 0;
+    }
+    count = sum_of_wave(count);
+    if (lane == 0) reached_by[step & 1][wave] = count;
+    __syncthreads();  // (the next step writes the other half, so one is enough)
+    const int* of = reached_by[step & 1];
+    count = (of[0] + of[1]) + (of[2] + of[3]);
+    if (count >= a.n) {
+      lo = mid;
+      few = count <= kSelectRanked;
+    } else {
+      hi = mid;
+    }
+    mid = step == 0 ? lo + 1u : lo + (hi - lo) / 2u;
+  }
+  // elements that reach lo, if they are few, else those above it: fewer than n (a comparison of
+  // floats, to which zeros of both signs are equal)
+  const float equal = from_order(lo);
+  __shared__ int equals[NV][4];
+  __syncthreads();  // the lists' first form is read
+  if (tid == 0) listed = 0;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    v[j].again();
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const float f = v[j].at(i);
+      if (few ? f >= equal : f > equal) {
+        const int place = atomicAdd(&listed, 1);
+        list[place] = select_key(f, e0 + j * kBlock + i);
+      }
+      count += f == equal ? 1 : 0;
+    }
+    count = sum_of_wave(count);
+    if (lane == 0) equals[j][wave] = count;
+  }
+  __syncthreads();
+  const int above = listed;
+  for (int i = tid / kRankLanes; i < above; i += kSelectThreads / kRankLanes) {
+    const unsigned long long key = list[i];
+    int rank = 0;
+    for (int k = tid % kRankLanes; k < above; k += kRankLanes) rank += list[k] > key ? 1 : 0;
+    rank = sum_of_eight(rank);
+    if (rank < a.n && tid % kRankLanes == 0) out[rank] = key;
+  }
+  if (few) return;
+  // equal ones by token: by block, then lane, then place in the lane's load
+  int rank0 = above;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    int rank = rank0;
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) rank += equals[j][w];
+      rank0 += equals[j][w];
+    }
+    if (rank >= a.n) continue;
+    v[j].again();
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const unsigned long long same = __ballot(v[j].at(i) == equal);
+      rank += __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
     }
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      const unsigned long long other = __shfl_xor(best, off, 64);
-      best = other > best ? other : best;
-    }
-    __syncthreads();  // the last round's are read
-    if (lane == 0) wave_best[wave] = best;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 4; ++w) best = wave_best[w] > best ? wave_best[w] : best;
-    if (tid == 0) out[r] = best;
-    last = best;
+    for (int i = 0; i < kVec; ++i)
+      if (v[j].at(i) == equal) {
+        if (rank < a.n) out[rank] = select_key(equal, e0 + j * kBlock + i);
+        ++rank;
+      }
   }
 }
 

@@ -104,3 +104,46 @@ def crowded(kind, seed, G, K, V, dtype):
 def test_every_rank_of_crowded_rows(G, K, V, n, kind, dtype):
     x, scores = crowded(kind, n, G, K, V, dtype)
     check_ranks(x, scores, None, -1, n, dtype)
+
+
+def event_time(call, passes=5):
+    """The least of some passes, so that one that is held up does not count."""
+    call()
+    marks = [torch.cuda.Event(enable_timing=True) for _ in range(passes + 1)]
+    torch.cuda.synchronize()
+    marks[0].record()
+    for m in marks[1:]:
+        call()
+        m.record()
+    torch.cuda.synchronize()
+    return min(a.elapsed_time(b) for a, b in zip(marks, marks[1:]))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kind", ["mask_lowest", "mask_1e4", "flat", "near", "steps", "equal"])
+def test_crowded_rows_are_not_read_once_a_candidate(kind, dtype):
+    """Their pieces are in registers already: where the lists overflow, the bound is raised there.  (16
+    candidates by 16 passes over memory took 20 times the ordinary rows' time; up to 33 counts of
+    registers take a few times it at most.)"""
+    G, K, V, n = 64, 8, 65_536, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((G * K, V), generator=g, device="cuda") * 2.5
+    plain = x.to(dtype)
+    if kind.startswith("mask"):
+        keep = torch.rand(x.shape, generator=g, device="cuda") < 20 / V
+        x = torch.where(keep, x, torch.finfo(dtype).min if kind == "mask_lowest" else -1e4)
+    elif kind == "flat":
+        x = -11.77 + 0.008 * x
+    elif kind == "near":
+        x = 5.0 + torch.randint(0, 1 << 14, x.shape, generator=g, device="cuda") * 2.0 ** -21
+    elif kind == "steps":
+        x = x.floor()
+    else:
+        x = torch.full_like(x, 1.25)
+    crowd = x.to(dtype)
+    scores = -torch.rand((G, K), generator=g, device="cuda")
+    out = [torch.empty((G, n), dtype=t, device="cuda") for t in (torch.int32, torch.int32, torch.float32)]
+    work = torch.empty(eng.engram_beam_select_workspace(G, K, V, n), dtype=torch.uint8, device="cuda")
+    times = [event_time(lambda: eng.engram_beam_select(t, scores, *out, workspace=work)) for t in (plain, crowd)]
+    assert status() == 0
+    assert times[1] <= 8 * times[0], times
