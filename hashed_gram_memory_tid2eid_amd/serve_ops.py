@@ -29,10 +29,12 @@ except ImportError as e:
 
 _I32, _I64, _U8, _F32 = torch.int32, torch.int64, torch.uint8, torch.float32
 _LOGITS = {torch.bfloat16: ENGRAM_DTYPE_BF16, torch.float32: ENGRAM_DTYPE_F32}
+# (looked up once: 0.1 us a call; a torch without it may still be imported)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _raw(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    return _raw_stream(dev) if stream is None else _stream(stream)
 
 
 def _count(n, name):
