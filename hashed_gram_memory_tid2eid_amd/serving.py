@@ -14,7 +14,7 @@ DeepseekV4Model.__init__: the hash state is keyed by the KV cache's slots).
     d.prefill(tokens, streams)          # the n-gram memory of the prompts
     ...                                 # the model, whose cache rows are d.token_slots
     d.first(logits)                     # [G][V] at the prompts' last tokens: every request's K beams
-    for ...:
+    for _ in range(d.max_len - longest):  # at most, until all of d.done
         d.plan()                        # a place for one more token a beam
         d.step(streams)                 # the n-gram memory of d.tokens
         ...                             # the model
@@ -35,6 +35,11 @@ class BeamDecode:
     pages; they are copied where beams part inside a page.  ``num_pages`` defaults to a whole
     table for every beam; it may be less, since the beams of a request share what they have in
     common.  ``stream``: that of the first calls, behind all that the current stream holds.
+    ``max_len``: tokens of a beam, prompt and all, rounded up to whole pages: the attribute max_len
+    is what plan keeps to, and what a model's positions have to reach.
+
+    All requests go on together, ended ones too (they take a place a step until finish), and plan
+    refuses every beam where one would pass max_len: take it for the longest prompt and all steps.
 
     Buffers on the device: tokens, parents, slots, scores, done [requests][beams]; lens and tables,
     a row a beam; free, the pool.  Of the last plan: cu_seqlens, seq_start, token_slots and
@@ -54,9 +59,10 @@ class BeamDecode:
             raise ValueError(f"{n} beams > the runner's max_tokens {engram.max_tokens}")
         self.engram, self.requests, self.beams, self.page_size = engram, G, K, page_size
         self.blocks = -(-max_len // page_size)
+        self.max_len = self.blocks * page_size
         self.num_pages = n * self.blocks if num_pages is None else int(num_pages)
         self.end_token, self.caches = end_token, list(caches)
-        self.max_prompt_tokens = G * max_len if max_prompt_tokens is None else int(max_prompt_tokens)
+        self.max_prompt_tokens = G * self.max_len if max_prompt_tokens is None else int(max_prompt_tokens)
         places = max(self.max_prompt_tokens, n)
         i32 = dict(dtype=torch.int32, device="cuda")
         self.store = None if engram is None else engram.make_store(n, stream=stream)

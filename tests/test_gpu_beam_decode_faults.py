@@ -93,3 +93,24 @@ def test_caches_that_cannot_be_copied_are_refused_when_made():
     d.start(dev([1, 1]), 2)
     d.first(torch.zeros((2, 10), device="cuda"))
     assert status() == 0
+
+
+# ---------------------------------------------------------------------------
+# lengths
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("max_len, P, holds", [(17, 16, 32), (16, 16, 16), (1, 1, 1), (5, 3, 6)])
+def test_max_len_is_what_plan_keeps_to(max_len, P, holds):
+    d = eng.BeamDecode(None, requests=2, beams=2, max_len=max_len, page_size=P, vocab=10)
+    assert d.max_len == holds
+    d.start(dev([holds, 1]), holds + 1)
+    d.finish()
+    d.start(dev([1, 1]), 2)
+    d.first(torch.zeros((2, 10), device="cuda"))
+    for i in range(holds - 1):
+        d.plan()
+        assert d.positions.tolist() == [i + 1] * 4
+        d.select(torch.zeros((4, 10), device="cuda"))
+    assert status() == 0
+    d.plan()
+    assert status() == eng.ENGRAM_E_SEQLENS and d.lens.tolist() == [holds] * 4
