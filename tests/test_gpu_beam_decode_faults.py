@@ -114,3 +114,29 @@ def test_max_len_is_what_plan_keeps_to(max_len, P, holds):
     assert status() == 0
     d.plan()
     assert status() == eng.ENGRAM_E_SEQLENS and d.lens.tolist() == [holds] * 4
+
+
+def test_the_loop_of_the_readme_ends():
+    """As it stands there, with a request that has nothing to select from (its beams are never done)."""
+    import os
+    import re
+
+    import engram_inputs as ei
+    from engram_harness import DEV, Site
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "README.md")) as f:
+        code = next(c for c in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "BeamDecode(" in c)
+    cfg = ei.get_config("decode_tiny")
+    lens = [4085, 4070, 3, 1, 77, 4085, 16, 2]
+    total = sum(lens)
+    logits = torch.randn((32, 129_280), device="cuda")
+    logits[:, cfg.vocab:] = -torch.inf
+    logits[8:12] = torch.nan
+    names = dict(engram=Site(cfg, max_tokens=total).site, kv=torch.zeros((8 * 4 * 256, 16), device="cuda"),
+                 prompt_lens=dev(lens), num_tokens=total, longest_prompt=max(lens),
+                 prompt_tokens=torch.zeros(total, dtype=torch.int32, device="cuda"),
+                 prompt_streams=ei.make_streams(cfg, total, DEV), streams=ei.make_streams(cfg, 32, DEV), logits=logits,
+                 prompt_logits=logits[::4].contiguous())
+    exec(code, names)
+    d = names["d"]
+    assert status() == 0 and all_free(d) and not d.done[2].any()
