@@ -137,8 +137,10 @@ extern "C" int engram_beam_reorder(const int32_t* d_parents, int32_t G, int32_t 
                                    int64_t table_ld, int32_t max_blocks, const int32_t* d_lens, int32_t page_size,
                                    uint32_t* d_free, int32_t num_pages, int32_t* d_page_src, int32_t* d_page_dst,
                                    hipStream_t stream) {
-  if (G < 0 || K < 1 || (!d_slots && !d_tables)) return ENGRAM_E_ARG;
+  if (G < 0 || K < 1) return ENGRAM_E_ARG;
   if (K > 64 || (int64_t)G * K > 1 << 20) return ENGRAM_E_UNSUPPORTED;
+  if (G == 0) return ENGRAM_OK;  // (arrays without entries may be null)
+  if (!d_slots && !d_tables) return ENGRAM_E_ARG;
   if (d_slots ? !d_slots_out : (store || d_slots_out || d_slot_src || d_slot_dst)) return ENGRAM_E_ARG;
   if (store) {
     const int rc = engram::store_usable(store, nullptr);
@@ -153,7 +155,6 @@ extern "C" int engram_beam_reorder(const int32_t* d_parents, int32_t G, int32_t 
   } else if (d_tables_out || d_free || d_page_src || d_page_dst) {
     return ENGRAM_E_ARG;
   }
-  if (G == 0) return ENGRAM_OK;
   if (!d_parents) return ENGRAM_E_ARG;
   for (const void* p : {(const void*)d_parents, (const void*)d_slots, (const void*)d_slots_out, (const void*)d_slot_src,
                         (const void*)d_slot_dst, (const void*)d_tables, (const void*)d_tables_out, (const void*)d_lens,
