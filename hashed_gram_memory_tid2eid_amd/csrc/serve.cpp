@@ -207,7 +207,7 @@ extern "C" int engram_state_copy(void* d_state, int64_t planes, int64_t plane_pi
   if (planes > kMaxGroups || (int64_t)n * planes > kMaxGroups) return ENGRAM_E_UNSUPPORTED;
   if (!rows_apart(planes, plane_pitch, rows, row_pitch, row_bytes)) return ENGRAM_E_ARG;
   if (n == 0 || planes == 0) return ENGRAM_OK;
-  if (!d_state || !d_src || !d_dst) return ENGRAM_E_ARG;
+  if ((!d_state && rows > 0) || !d_src || !d_dst) return ENGRAM_E_ARG;
   if (!aligned(d_src, 4) || !aligned(d_dst, 4)) return ENGRAM_E_ALIGN;
   engram::StateCopyArgs a = {};
   a.state = static_cast<char*>(d_state);

@@ -39,3 +39,13 @@ def test_release_of_no_rows():
     words = dev([5])
     eng.engram_block_release(zeros(0, 4), zeros(0), zeros(0, dtype=torch.uint8), words, page_size=4, num_pages=20)
     assert status() == 0 and words.tolist() == [5]
+
+
+@pytest.mark.parametrize("shape", [(0, 8), (3, 0, 8), (0, 5, 8), (3, 5, 0)])
+def test_copy_of_a_state_without_rows(shape):
+    state = torch.zeros(shape, device="cuda")
+    eng.engram_state_copy(state, dev([-1, 3, 0]), dev([0, -1, 0]))
+    assert status() == 0
+    if shape[-2] == 0 and 0 not in shape[:-2]:
+        eng.engram_state_copy(state, dev([1]), dev([2]))
+        assert status() == eng.ENGRAM_E_SLOT_RANGE
