@@ -6,7 +6,9 @@
 // ballot is empty, in order.  A block table is then permuted a tile of 256 columns at a time
 // through LDS, so that in place and out of place are the same code.  A page of a full block is
 // freed where a beam that no row continues names it and no continued one does; both are at the
-// same column, which is where beams of one request share pages.
+// same column, which is where beams of one request share pages.  512 requests of 8 beams, 1,024
+// blocks: 8.5 us, with store entries 8.6 (slots alone 3.0 and 3.4): the parents and lengths, then
+// the columns, then the stores, each waiting for the last.
 
 namespace engram {
 
@@ -159,7 +161,8 @@ hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t stream) {
 // takes, up to a workgroup, which then takes one piece of it; a pair's planes by neighbouring
 // workgroups.  Bound by memory: 256 pairs of 16 KB in 32 planes, 268 MB, 51 us (5.3 TB/s).  Plane
 // by plane 55; ordinary stores 60; loads past the caches, too, 54; one unit a lane 62; 2,048
-// workgroups that go on from item to item 62.
+// workgroups that go on from item to item 62.  Units of 4 and of 1 byte (one state, part of it in
+// the last cache): 46 us for rows of 16,380 bytes, 174 for 16,383, against 37.6 for 16,384.
 
 constexpr int kCopyThreads = 256;
 typedef uint32_t copy16_t __attribute__((ext_vector_type(4)));

@@ -19,9 +19,11 @@
 // The second launch, one workgroup a request, adds the pieces' sums in 64 bits, turns the keys
 // into totals and selects among them by the same bound, list and count.
 //
-// Bound by memory where rows are many (2,048 x 129,280 fp32: 152 us, 7.0 TB/s in the first launch;
-// bf16 80 us, 6.0 TB/s), by latency below (4 rows 8.8 us, 512 rows of 65,537 bf16 22.2: their
-// pieces all load, then all compute).
+// Bound by memory where rows are many (2,048 x 129,280 fp32, 5% of them ended: 152 us, 7.0 TB/s in
+// the first launch; bf16, 10% ended, 80 us, 6.0 TB/s), by latency below (4 rows 8.8 us, 512 rows
+// of 65,537 bf16 22.2: their pieces all load, then all compute).  Where a mask's value or a flat row
+// raises the bounds, the counts are on top: 2,048 x 129,280 masked by the lowest value, none
+// ended, fp32 251 us, bf16 161 (161 and 91 without the mask).
 
 namespace engram {
 
@@ -38,7 +40,8 @@ static_assert(kFewLoads * 8 <= kSelectRanked && kSelectRanked <= kSelectList, "w
 constexpr int kRankLanes = 8;      // lanes that count the larger ones of one element together
 // Up to so many of 64 values the n-th largest is a good bound: some 45 elements reach it where n
 // is 32.  All 64 are reached by hundreds, so more of them take 256 values (64 candidates of 64 x
-// 16 rows of 65,536 bf16: 778 us by 64, most of them one by one because the lists overflow).
+// 16 rows of 65,536 bf16: 40.5 us by 256, 94 by 64, most of whose bounds are raised again; 33
+// candidates 32.2 and 31.0).
 constexpr int kFewCandidates = 32;
 constexpr int kMergeList = 2048;
 constexpr float kLowest = -3.402823466e38f;
@@ -480,7 +483,10 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
     double z = 0.0;
     for (int i = at; i < S; i += 64) {
       if (i >= 64) p = part[i];
-      // a piece's sum is of 2^(x log2e - c), with the constant as fp32 has it
+      // a piece's sum is of 2^(x log2e - c), with the constant as fp32 has it.  Its scale 2^(d log2e),
+      // d <= 0, is an exponential of fp32: a unit of its own, and 2^-24 |d| each of the difference's
+      // and the product's rounding.  They count e^d times: some 2^-23 of the whole sum at most,
+      // no more than the piece's own exponentials are off
       const double shift = fabsf(p.x) < kFar ? (double)select_center(p.x) - (double)p.x * (double)kLog2e : 0.0;
       const float scale = __builtin_amdgcn_exp2f((p.x - m) * kLog2e);
       z += (double)p.y * (double)scale * (1.0 + shift * 0.6931471805599453);
@@ -574,7 +580,8 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
     for (int r = count + tid; r < n; r += THREADS) write_none(r);
     return;
   }
-  // too many equal ones: one by one, each the first behind the last
+  // too many that reach it (their totals agree in 12 bits of the mantissa): one by one, each the first behind the
+  // last (64 beams of 129,280 equal logits, 64 candidates: 189 us a call)
   __shared__ int wave_b[THREADS / 64];
   double last_t = INFINITY;
   unsigned long long last_k = 0;

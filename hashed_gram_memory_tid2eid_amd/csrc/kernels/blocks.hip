@@ -15,8 +15,8 @@ namespace engram {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWords = 8;                           // words of the bitmap a thread loads at a time
-// Up to so many pages are looked for one by one (4,096 of 64 rows 20 us, 8,192 32, 65,536 219),
-// more are handed out by the threads in whose words they are (28, 29, 50).
+// Up to so many pages are looked for one by one (4,096 of 64 rows 23.0 us, 6,144 28.6, 8,192 34.6,
+// 65,536 203), more are handed out by the threads in whose words they are (28.1, 28.7, 27.6, 48.5).
 constexpr uint32_t kPlanSearched = 6144;
 constexpr uint32_t kSat = 0x7FFFFFFFu;                  // sums stop here instead of wrapping round
 
@@ -392,8 +392,9 @@ __global__ __launch_bounds__(256) void block_tokens_kernel(PlanArgs a) {
   write_token(a, t, row, past, start);
 }
 
-// One workgroup does it all for up to 4,096 tokens (64 rows: 9.8 us either way; 2,048 tokens 8.2
-// against 9.5, 8,192 tokens 13.4 against 10.2), or about a token a row (4,096 rows: 20 against 23).
+// One workgroup does it all for up to 4,096 tokens (64 rows: 9.5 us, two launches 9.3; 2,048 tokens
+// 8.1 against 9.2, 8,192 tokens 12.8 against 9.4), or about a token a row (2,048 rows 12.8 against
+// 17.4, 4,096 rows of 1M pages 15.3 against 18.8, 8,192 rows 22.6 against 24.6).
 constexpr int kPlanTokensHere = 4096;
 
 template <int TILES, int ROWS>
