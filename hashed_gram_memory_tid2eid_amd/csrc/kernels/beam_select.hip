@@ -17,7 +17,8 @@
 // until few enough reach it or it is the n-th largest logit itself, whose equals follow those
 // above it by their tokens.
 // The second launch, one workgroup a request, adds the pieces' sums in 64 bits, turns the keys
-// into totals and selects among them by the same bound, list and count.
+// into totals and selects among them by the same bound, list and count, with the bound raised
+// where many totals are nearly equal.
 //
 // Bound by memory where rows are many (2,048 x 129,280 fp32, 5% of them ended: 152 us, 7.0 TB/s in
 // the first launch; bf16, 10% ended, 80 us, 6.0 TB/s), by latency below (4 rows 8.8 us, 512 rows
@@ -32,8 +33,9 @@ constexpr int kSelectHeld = 4096;  // elements of the loads that hold one which 
 // Elements that reach it.  (Room past kSelectRanked leaves 5 workgroups of fp32 rows in a CU's LDS, which
 // read faster than more of them.)
 constexpr int kSelectList = 1024;
-// Up to so many are ranked (each reads all: 1,024 of them, in each of 1,024 elements of a mask's
-// value, took 210 us); 64 candidates leave some 75, so that ordinary rows are below it.
+// Up to so many are ranked, each of which reads all.  64 candidates leave some 75, so that ordinary
+// rows are below it (16 x 64 rows of 65,536 bf16, n 64: 41 us, 171 by 64; 4 flat rows of 129,280
+// fp32, n 8: 13.9 us, 20.5 by 256, 200 by 1,024).
 constexpr int kSelectRanked = 128;
 constexpr int kFewLoads = 16;      // loads that one wave ranks; their elements cannot overflow the list
 static_assert(kFewLoads * 8 <= kSelectRanked && kSelectRanked <= kSelectList, "what one wave ranks is never too long");
@@ -43,7 +45,9 @@ constexpr int kRankLanes = 8;      // lanes that count the larger ones of one el
 // 16 rows of 65,536 bf16: 40.5 us by 256, 94 by 64, most of whose bounds are raised again; 33
 // candidates 32.2 and 31.0).
 constexpr int kFewCandidates = 32;
-constexpr int kMergeList = 2048;
+// The join ranks up to so many, and raises its bound above that (4 rows of 129,280 bf16, one token
+// allowed and the others -1e4, 8 candidates: 31 us, 263 where up to 2,048 were ranked).
+constexpr int kMergeRanked = 256;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.44269504088896341f;
 
@@ -425,6 +429,16 @@ __device__ __forceinline__ double beam_total(const MergeBeams& s, int b, unsigne
   return (s.score[b] + ((double)key_logit(key) - s.most[b])) - s.norm[b];
 }
 
+// The order of candidates in two whole numbers: totals (-0 as 0), and among equal ones lower beams,
+// larger logits, lower tokens (of 24 bits).
+__device__ __forceinline__ unsigned long long total_in_order(double t) {
+  const unsigned long long b = (unsigned long long)__double_as_longlong(t + 0.0);
+  return (b >> 63) != 0 ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ unsigned long long place_in_order(int b, unsigned long long key) {
+  return (unsigned long long)(63 - b) << 56 | (key >> 32) << 24 | (key & 0xFFFFFFu);
+}
+
 __device__ __forceinline__ bool goes_before(double ta, int ba, unsigned long long ka, double tb, int bb,
                                             unsigned long long kb) {
   return ta > tb || (ta == tb && (ba < bb || (ba == bb && ka > kb)));
@@ -437,9 +451,9 @@ template <int THREADS>
 __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a) {
   __shared__ MergeBeams beams;
   __shared__ uint32_t slot_max[256];
-  __shared__ double totals[kMergeList];
-  __shared__ unsigned long long keys[kMergeList];
-  __shared__ uint8_t of_beam[kMergeList];
+  __shared__ double totals[kMergeRanked];
+  __shared__ unsigned long long keys[kMergeRanked];
+  __shared__ uint8_t of_beam[kMergeRanked];
   __shared__ int listed;
   const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int S = a.splits, K = a.K, n = a.n;
@@ -523,7 +537,7 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
 
   auto push = [&](double total, int b, unsigned long long key) {
     const int place = atomicAdd(&listed, 1);
-    if (place < kMergeList) {
+    if (place < kMergeRanked) {
       totals[place] = total;
       keys[place] = key;
       of_beam[place] = (uint8_t)b;
@@ -565,82 +579,125 @@ __global__ __launch_bounds__(THREADS) void beam_select_merge_kernel(SelectArgs a
     a.out_scores[at] = -INFINITY;
     if (a.out_done != nullptr) a.out_done[at] = 0;
   };
-  const int count = listed;
-  if (count <= kMergeList) {
-    for (int i = tid / kRankLanes; i < count; i += THREADS / kRankLanes) {
-      const double total = totals[i];
-      const unsigned long long key = keys[i];
-      const int b = of_beam[i];
-      int rank = 0;
-      for (int k = tid % kRankLanes; k < count; k += kRankLanes)
-        rank += goes_before(totals[k], of_beam[k], keys[k], total, b, key) ? 1 : 0;
-      rank = sum_of_eight(rank);
-      if (rank < n && tid % kRankLanes == 0) write(rank, total, b, key);
-    }
-    for (int r = count + tid; r < n; r += THREADS) write_none(r);
-    return;
-  }
-  // too many that reach it (their totals agree in 12 bits of the mantissa): one by one, each the first behind the
-  // last (64 beams of 129,280 equal logits, 64 candidates: 189 us a call)
-  __shared__ int wave_b[THREADS / 64];
-  double last_t = INFINITY;
-  unsigned long long last_k = 0;
-  int last_b = -1;
-  for (int r = 0; r < n; ++r) {
-    double best_t = -INFINITY;
-    unsigned long long best_k = 0;
-    int best_b = -1;
-    auto consider = [&](double t, int b, unsigned long long key) {
-      if (goes_before(last_t, last_b, last_k, t, b, key) &&
-          (best_b < 0 || goes_before(t, b, key, best_t, best_b, best_k))) {
-        best_t = t;
-        best_k = key;
-        best_b = b;
-      }
+  int count = listed;
+  if (count > kMergeRanked) {
+    // Totals that agree in the bound's bits, as those of masked tokens do.  The bound is raised by
+    // bisection, counting again, until few reach it or it is the n-th largest total, and then among
+    // the candidates of that total by their places, which are all different.
+    __shared__ int counts[2][THREADS / 64];
+    __shared__ unsigned long long ends[2][THREADS / 64];
+    int turn = 0;
+    auto count_all = [&](int c) {
+      c = sum_of_wave(c);
+      if (lane == 0) counts[turn][wave] = c;
+      __syncthreads();  // (the next count writes the other half, so one is enough)
+      int sum = 0;
+      for (int w = 0; w < THREADS / 64; ++w) sum += counts[turn][w];
+      turn ^= 1;
+      return sum;
     };
-    for (int i = tid; i < places; i += THREADS) {
-      const int b = i / n / S;
-      if (beams.kind[b] != 1) continue;
-      const unsigned long long key = all[i];
-      if (key != 0) consider(beam_total(beams, b, key), b, key);
-    }
-    if (tid < K && beams.kind[tid] == 2) consider(beams.score[tid], tid, select_key(0.0f, a.end_token));
-    auto join = [&](double t, int b, unsigned long long key) {
-      if (b >= 0 && (best_b < 0 || goes_before(t, b, key, best_t, best_b, best_k))) {
-        best_t = t;
-        best_k = key;
-        best_b = b;
-      }
-    };
+    // candidates whose totals reach `least`
+    auto each = [&](unsigned long long least, auto f) {
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      const double t = __shfl_xor(best_t, off, 64);
-      const unsigned long long key = __shfl_xor(best_k, off, 64);
-      const int b = __shfl_xor(best_b, off, 64);
-      join(t, b, key);
-    }
-    __syncthreads();  // the last round's are read
-    if (lane == 0) {
-      totals[wave] = best_t;
-      keys[wave] = best_k;
-      wave_b[wave] = best_b;
-    }
+      for (int q = 0; q < kMergeKeys; ++q)
+        if (mine[q] != 0 && total_in_order(total[q]) >= least) f(total[q], piece_of[q], mine[q]);
+      if (places > kMergeKeys * THREADS) {
+        for (int piece = tid; piece < pieces; piece += THREADS) {
+          const int b = piece / S;
+          if (beams.kind[b] != 1) continue;
+          const int known = piece < kMergeKeys * THREADS ? (kMergeKeys * THREADS - piece + pieces - 1) / pieces : 0;
+          for (int order = known; order < n; ++order) {
+            const unsigned long long key = all[(int64_t)piece * n + order];
+            if (key == 0) break;
+            const double t = beam_total(beams, b, key);
+            if (total_in_order(t) < least) break;
+            f(t, b, key);
+          }
+        }
+      }
+      if (tid < K && beams.kind[tid] == 2 && total_in_order(beams.score[tid]) >= least)
+        f(beams.score[tid], tid, select_key(0.0f, a.end_token));
+    };
+    // the least lo and the largest hi of the workgroup
+    auto ends_of = [&](unsigned long long& lo, unsigned long long& hi) {
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) {
+        const unsigned long long l = __shfl_xor(lo, off, 64), h = __shfl_xor(hi, off, 64);
+        lo = l < lo ? l : lo;
+        hi = h > hi ? h : hi;
+      }
+      __syncthreads();  // earlier ends are read
+      if (lane == 0) ends[0][wave] = lo, ends[1][wave] = hi;
+      __syncthreads();
+      for (int w = 0; w < THREADS / 64; ++w) {
+        lo = ends[0][w] < lo ? ends[0][w] : lo;
+        hi = ends[1][w] > hi ? ends[1][w] : hi;
+      }
+    };
+    // lo, which at least `want` of the visited numbers reach, is raised below hi, which `above` do,
+    // fewer: until at most `room` reach it (true), or it is the want-th largest itself.  Numbers lie
+    // in clusters (the totals of a beam's masked tokens, the places of a beam), so both ends go
+    // to the next numbers now and then.
+    auto raise = [&](unsigned long long& lo, int first, int want, int room, int& above, auto visit) {
+      unsigned long long hi = ~0ull, mid = 0;
+      above = 0;
+      for (int step = 0;; ++step) {
+        if (step % 8 == 0) {
+          unsigned long long l = ~0ull, h = 0;
+          visit(lo, [&](unsigned long long v) {
+            if (v < lo || v >= hi) return;
+            l = v < l ? v : l;
+            h = v > h ? v : h;
+          });
+          ends_of(l, h);
+          lo = l;
+          hi = h + 1;
+          mid = step == 0 ? lo + first : lo + (hi - lo) / 2;
+        }
+        if (hi <= lo || hi - lo == 1) return false;
+        int c = 0;
+        visit(mid, [&](unsigned long long v) { c += v >= mid ? 1 : 0; });
+        c = count_all(c);
+        if (c >= want) {
+          lo = mid;
+          if (c <= room) return true;
+        } else {
+          hi = mid;
+          above = c;
+        }
+        mid = lo + (hi - lo) / 2;
+      }
+    };
+    unsigned long long cut = (unsigned long long)bound << 32, place = 0;
+    int above, ahead;
+    // (the first step asks whether the least total is the n-th itself)
+    if (!raise(cut, 1, n, kMergeRanked, above, [&](unsigned long long least, auto f) {
+          each(least, [&](double t, int, unsigned long long) { f(total_in_order(t)); });
+        }))
+      raise(place, 0, n - above, kMergeRanked - above, ahead, [&](unsigned long long, auto f) {
+        each(cut, [&](double t, int b, unsigned long long key) {
+          if (total_in_order(t) == cut) f(place_in_order(b, key));
+        });
+      });
+    if (tid == 0) listed = 0;
     __syncthreads();
-    for (int w = 0; w < THREADS / 64; ++w) join(totals[w], wave_b[w], keys[w]);
-    if (tid == 0) {
-      if (best_b >= 0)
-        write(r, best_t, best_b, best_k);
-      else
-        write_none(r);
-    }
-    if (best_b < 0) {  // nothing is left (best_* are the same in every thread)
-      for (int q = r + 1 + tid; q < n; q += THREADS) write_none(q);
-      return;
-    }
-    last_t = best_t;
-    last_k = best_k;
-    last_b = best_b;
+    each(cut, [&](double t, int b, unsigned long long key) {
+      if (total_in_order(t) != cut || place_in_order(b, key) >= place) push(t, b, key);
+    });
+    __syncthreads();
+    count = listed;
   }
+  for (int i = tid / kRankLanes; i < count; i += THREADS / kRankLanes) {
+    const double total = totals[i];
+    const unsigned long long key = keys[i];
+    const int b = of_beam[i];
+    int rank = 0;
+    for (int k = tid % kRankLanes; k < count; k += kRankLanes)
+      rank += goes_before(totals[k], of_beam[k], keys[k], total, b, key) ? 1 : 0;
+    rank = sum_of_eight(rank);
+    if (rank < n && tid % kRankLanes == 0) write(rank, total, b, key);
+  }
+  for (int r = count + tid; r < n; r += THREADS) write_none(r);
 }
 
 // ---------------------------------------------------------------------------

@@ -106,6 +106,32 @@ def test_every_rank_of_crowded_rows(G, K, V, n, kind, dtype):
     check_ranks(x, scores, None, -1, n, dtype)
 
 
+def narrow(kind, seed, G, K, V, dtype):
+    """Rows masked by a finite number but for few tokens, so that masked ones are among the n best."""
+    x, scores = select_inputs(seed, G, K, V)
+    keep = np.zeros(V, dtype=bool)
+    keep[[V // 3] if kind.endswith("1") else [0, V // 2, V - 1]] = True
+    x[:, ~keep] = torch.finfo(dtype).min if kind.startswith("lowest") else -1e4
+    if kind == "1e4_same":  # the same total for every masked token of every beam
+        x[:] = x[0]
+        scores[:] = -1.0
+    return x, scores
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("ended", [False, True])
+@pytest.mark.parametrize("kind", ["lowest_1", "lowest_3", "1e4_1", "1e4_3", "1e4_same"])
+@pytest.mark.parametrize("G, K, V, n", [(1, 4, 129_280, 8), (3, 8, 20_001, 64), (40, 8, 8193, 16), (2, 64, 9001, 64), (1, 64, 129_280, 64),
+                                        (1, 1, 500_000, 64)])
+def test_every_rank_of_narrow_choices(G, K, V, n, kind, ended, dtype):
+    x, scores = narrow(kind, n, G, K, V, dtype)
+    done = None
+    if ended:
+        done = (np.random.default_rng(V).random((G, K)) < 0.3).astype(np.uint8)
+        scores[:, K // 2:] -= 3.0
+    check_ranks(x, scores, done, V - 1 if ended else -1, n, dtype)
+
+
 def event_time(call, passes=5):
     """The least of some passes, so that one that is held up does not count."""
     call()
@@ -147,3 +173,22 @@ def test_crowded_rows_are_not_read_once_a_candidate(kind, dtype):
     times = [event_time(lambda: eng.engram_beam_select(t, scores, *out, workspace=work)) for t in (plain, crowd)]
     assert status() == 0
     assert times[1] <= 8 * times[0], times
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("G, K, V, n", [(1, 4, 129_280, 8), (64, 8, 65_536, 16), (1, 64, 129_280, 64)])
+@pytest.mark.parametrize("mask", ["lowest", -1e4])
+def test_narrow_choices_are_not_joined_one_by_one(mask, G, K, V, n, dtype):
+    """One allowed token a row: totals of masked ones are equal and reach the join's bound.  (4 beams and
+    8 candidates took 100 times the ordinary rows' time.)"""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    plain = (torch.randn((G * K, V), generator=g, device="cuda") * 2.5).to(dtype)
+    crowd = torch.full_like(plain, torch.finfo(dtype).min if mask == "lowest" else mask)
+    crowd[:, 77] = plain[:, 77]
+    scores = -torch.rand((G, K), generator=g, device="cuda")
+    out = [torch.empty((G, n), dtype=t, device="cuda") for t in (torch.int32, torch.int32, torch.float32)]
+    work = torch.empty(eng.engram_beam_select_workspace(G, K, V, n), dtype=torch.uint8, device="cuda")
+    times = [event_time(lambda: eng.engram_beam_select(t, scores, *out, workspace=work)) for t in (plain, crowd)]
+    assert status() == 0
+    # (an event's time of a call this short holds some 10 us of its own)
+    assert times[1] <= 8 * times[0] + 0.02, times
