@@ -192,3 +192,39 @@ def test_narrow_choices_are_not_joined_one_by_one(mask, G, K, V, n, dtype):
     assert status() == 0
     # (an event's time of a call this short holds some 10 us of its own)
     assert times[1] <= 8 * times[0] + 0.02, times
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_one_graph_of_ordinary_and_crowded_rows(dtype):
+    """Captured with ordinary logits, replayed with others, on a stream of its own, with eager work
+    between the replays."""
+    G, K, V, n = 5, 4, 40_003, 8
+    inputs = [select_inputs(1, G, K, V)[0]] + [crowded(kind, 2, G, K, V, dtype)[0] for kind in ("mask_lowest", "flat", "equal")]
+    inputs += [narrow(kind, 3, G, K, V, dtype)[0] for kind in ("lowest_1", "1e4_3")] + [select_inputs(4, G, K, V)[0]]
+    inputs = [torch.as_tensor(x, device="cuda").to(dtype) for x in inputs]
+    scores = -torch.rand((G, K), device="cuda")
+    work = torch.empty(eng.engram_beam_select_workspace(G, K, V, n), dtype=torch.uint8, device="cuda")
+
+    def outputs():
+        return [torch.empty((G, n), dtype=t, device="cuda") for t in (torch.int32, torch.int32, torch.float32)]
+
+    want = []
+    for x in inputs:
+        want.append(outputs())
+        eng.engram_beam_select(x, scores, *want[-1], workspace=work)
+    logits, out = inputs[0].clone(), outputs()
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        eng.engram_beam_select(logits, scores, *out, workspace=work)
+    for i in (1, 0, 2, 3, 5, 4, 6, 1):
+        logits.copy_(inputs[i])
+        for o in out:
+            o.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        torch.randn(1000, device="cuda").sum().item()
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want[i])), i
+    assert status() == 0
