@@ -52,6 +52,8 @@ class BeamDecode:
         import torch
         if requests < 1 or not 1 <= beams <= 64 or max_len < 1 or page_size < 1:
             raise ValueError("requests, max_len and page_size must be positive, beams 1 to 64")
+        if not -1 <= end_token < vocab:
+            raise ValueError("end_token must be a token of the vocabulary, or -1")
         G, K, n = requests, beams, requests * beams
         if n > 8192:
             raise ValueError("at most 8,192 beams in all")

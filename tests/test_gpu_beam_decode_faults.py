@@ -140,3 +140,14 @@ def test_the_loop_of_the_readme_ends():
     exec(code, names)
     d = names["d"]
     assert status() == 0 and all_free(d) and not d.done[2].any()
+
+
+@pytest.mark.parametrize("end_token", [10, 11, -2])
+def test_an_end_token_outside_the_vocabulary_is_refused_when_made(end_token):
+    size = dict(requests=2, beams=2, max_len=8, page_size=2, vocab=10)
+    with pytest.raises(ValueError):
+        eng.BeamDecode(None, end_token=end_token, **size)
+    d = eng.BeamDecode(None, end_token=9, **size)
+    d.start(dev([1, 1]), 2)
+    d.first(torch.zeros((2, 10), device="cuda"))
+    assert status() == 0
